@@ -1,0 +1,475 @@
+"""The AdamW operators over many tensors at once, with their moments in 32 or
+in 8 bits, as measured calls: their inputs, their plain form in torch and the
+framework's own calls.
+
+A parameter set is either a plan's (flat arrays, gradients in bucket buffers,
+reduced over the rank slots and accumulated first) or a group of tensors that
+stay where they lie.  8-bit moments are held in blocks of 64 elements:
+  m as e4m3 codes of 256 * m / s, s the block's largest |m|;
+  sqrt(v) as unsigned floats of 4 exponent and 4 mantissa bits (FP16's bits
+  6 to 13) of sqrt(v) / s, s the block's largest sqrt(v).
+"""
+import functools
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEVICE = "cuda"
+BLOCK = 64
+LR, BETA1, BETA2, EPS, DECAY, MAX_NORM, STEP = 1e-3, 0.9, 0.999, 1e-8, 0.01, 1.0, 100
+SIGMA = 1e-2
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+PLACEMENTS = ("replicate", "partial", "shard", "reduced")
+BIG = 167_391_488          # a 1/8 flat shard of a 1B-class dense model
+DRAFT = 67_118_592         # a 4-layer draft model of width 1024
+HYBRID = 298_983_326       # 4000 tensors of a mixture of experts
+
+
+# ------------------------------------------------------------------- cases
+def listed():
+    return [
+        # a step with 8-bit moments of a handful of small tensors: latency
+        {"name": "plan8 tiny", "kind": "plan8", "set": "tiny", "elements": 96_409, "tensors": 10, "R": 2, "window": 1,
+         "fp32_grad": False, "bf16": True},
+        # the draft model's step: window of 4 microbatches, rank contributions of 2, BF16 copy
+        {"name": "plan8 draft", "kind": "plan8", "set": "draft", "elements": DRAFT, "tensors": 34, "R": 2, "window": 4,
+         "fp32_grad": False, "bf16": True},
+        # a flat FSDP shard whose gradients an earlier owner has reduced, in FP32: no BF16 copy
+        {"name": "plan8 shard", "kind": "plan8", "set": "flat", "elements": BIG, "tensors": 1, "R": 1, "window": 1,
+         "fp32_grad": True, "bf16": False},
+        # a running job switched to 8-bit moments, or one restored from a checkpoint
+        {"name": "encode tiny", "kind": "encode", "set": "tiny", "elements": 96_409, "tensors": 10},
+        {"name": "encode shard", "kind": "encode", "set": "flat", "elements": BIG, "tensors": 1},
+        # 8-bit moments on their way into a checkpoint
+        {"name": "decode tiny", "kind": "decode", "set": "tiny", "elements": 96_409, "tensors": 10},
+        {"name": "decode draft", "kind": "decode", "set": "draft", "elements": DRAFT, "tensors": 34},
+        # norm weights and one small projection trained alone: latency
+        {"name": "group32 few", "kind": "group", "set": "random", "elements": 70_001, "tensors": 9, "state": "32",
+         "window": 1, "fp32_grad": True, "bf16": False, "sizes": 5},
+        # the draft model's tensors with BF16 gradients where backward left them
+        {"name": "group32 draft", "kind": "group", "set": "draft", "elements": DRAFT, "tensors": 34, "state": "32",
+         "window": 1, "fp32_grad": False, "bf16": True, "sizes": 0},
+        # the same with 8-bit moments
+        {"name": "group8 draft", "kind": "group", "set": "draft", "elements": DRAFT, "tensors": 34, "state": "8",
+         "window": 1, "fp32_grad": False, "bf16": True, "sizes": 0},
+        # thousands of tensors, the small ones' moments in 32 bits, gradients summed over 2 microbatches
+        {"name": "group mixed experts", "kind": "group", "set": "hybrid", "elements": HYBRID, "tensors": 4000,
+         "state": "mixed", "window": 2, "fp32_grad": False, "bf16": True, "sizes": 0},
+    ]
+
+
+def draw(rng):
+    kind = rng.choice(("plan8", "plan8", "encode", "decode", "group", "group", "group"))
+    n = int(math.exp(rng.uniform(math.log(1_000), math.log(DRAFT))))
+    case = {"kind": kind, "set": "random", "elements": n,
+            "tensors": min(n // 8, int(math.exp(rng.uniform(0.0, math.log(600))))), "sizes": rng.randrange(1 << 20)}
+    if kind == "plan8":
+        case.update(R=rng.choice((1, 2, 2, 3, 4)), window=rng.randint(1, 4), fp32_grad=rng.random() < 0.25,
+                    bf16=rng.random() < 0.75)
+        if case["fp32_grad"]:  # twice the gradient bytes: half the elements
+            case["elements"] = max(1_000, case["elements"] // 2)
+            case["tensors"] = min(case["tensors"], case["elements"] // 8)
+    elif kind == "group":
+        case.update(state=rng.choice(("32", "8", "mixed")), window=rng.randint(1, 4), fp32_grad=rng.random() < 0.25,
+                    bf16=rng.random() < 0.75)
+    return case
+
+
+def tensors_of(case):
+    """[(elements, placement, decayed)] in the order they are registered."""
+    if case["set"] == "tiny":
+        return [(65536, "shard", True), (256, "replicate", True), (16384, "shard", True), (64, "partial", True),
+                (64, "partial", True), (4096, "partial", True), (256, "replicate", True), (8192, "reduced", True),
+                (1000, "replicate", True), (561, "shard", True)]
+    if case["set"] == "draft":
+        h = 1024
+        layer = [(h, "replicate", False), (3 * h * h, "shard", True), (64, "partial", False), (64, "partial", False),
+                 (h * h, "shard", True), (h, "replicate", False), (4 * h * h, "shard", True), (4 * h * h, "shard", True)]
+        return [(16384 * h, "shard", True)] + 4 * layer + [(h, "replicate", False)]
+    if case["set"] == "flat":
+        return [(case["elements"], "replicate", True)]
+    if case["set"] == "hybrid":
+        raw = np.clip(np.round(np.exp(np.random.default_rng(3).normal(9.3, 2.0, size=4000))), 64, 4_194_304)
+        sizes = np.clip(np.round(raw * (300_000_000 / raw.sum())), 64, 4_194_304).astype(np.int64)
+        return [(int(s), "shard", bool(s >= 4096)) for s in sizes]
+    r = np.random.default_rng(case.get("sizes", 0))
+    k, n = case["tensors"], case["elements"]
+    share = np.exp(r.normal(0.0, 1.5, size=k))
+    sizes = np.maximum(1, np.floor(share / share.sum() * (n - k))).astype(np.int64)
+    sizes[int(np.argmax(sizes))] += n - int(sizes.sum())
+    return [(int(s), PLACEMENTS[int(r.integers(0, 4))], bool(r.random() < 0.8)) for s in sizes]
+
+
+def up(n):
+    return -(-n // BLOCK) * BLOCK
+
+
+def buckets_of(case):
+    """A plan's buckets, one for each owner class and decay setting: (slots, divisor, decayed, elements)."""
+    R = case.get("R", 1)
+    every = tensors_of(case)
+    found = []
+    for placement in PLACEMENTS:
+        for decayed in (True, False):
+            n = sum(t[0] for t in every if t[1] == placement and t[2] == decayed)
+            if n:
+                found.append((R if placement in ("replicate", "partial") else 1, R if placement == "replicate" else 1,
+                              decayed, n))
+    return found
+
+
+def work(case):
+    n, kind = case["elements"], case["kind"]
+    scales = 8 / BLOCK
+    if kind == "encode" or kind == "decode":
+        return {"bytes": n * (8 + 2 + scales), "flops": 12 * n}
+    grad = 4 if case["fp32_grad"] else 2
+    copy = 2 if case["bf16"] else 0
+    if kind == "plan8":
+        reads = sum(b[0] * b[3] for b in buckets_of(case)) * grad * case["window"]
+        return {"bytes": reads + n * (4 + 8 + 4 + 2 * scales + copy), "flops": 50 * n}
+    small = sum(t[0] for t in tensors_of(case) if in32(case, t))
+    return {"bytes": n * (grad + 8 + copy) + small * 16 + (n - small) * (4 + 2 * scales), "flops": 50 * n}
+
+
+# ------------------------------------------------------------------ inputs
+def normal(gen, *shape):
+    return torch.randn(shape, generator=gen, device=DEVICE, dtype=F32)
+
+
+def gradients(gen, slots, n, stride, dtype):
+    """Gradients whose size varies from run to run of 1024 elements; zeros behind the last one."""
+    rows = -(-stride // 1024)
+    size = (SIGMA * normal(gen, rows, 1).exp_()).expand(rows, 1024).reshape(-1)[:stride]
+    g = normal(gen, slots, stride).mul_(size)
+    g[:, n:] = 0
+    return g.to(dtype)
+
+
+def moments(gen, n, stride):
+    m, v = gradients(gen, 2, n, stride, F32)
+    return m.mul_(0.3).contiguous(), v.square_().contiguous()
+
+
+def weights(gen, n, stride):
+    p = normal(gen, stride).mul_(0.02)
+    p[n:] = 0
+    return p
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEVICE)
+    gen.manual_seed(seed)
+    return prepare_group(case, gen) if case["kind"] == "group" else prepare_plan(case, gen)
+
+
+def prepare_plan(case, gen):
+    kind = case["kind"]
+    buckets = buckets_of(case)
+    s = {"kind": kind}
+    both = [moments(gen, b[3], up(b[3])) for b in buckets]
+    m, v = torch.cat([x[0] for x in both]), torch.cat([x[1] for x in both])
+    del both
+    if kind == "encode":
+        s["m"], s["v"] = m, v
+        s["m8"], s["v8"] = (torch.zeros(m.numel(), dtype=torch.uint8, device=DEVICE) for _ in "mv")
+        s["ms"], s["vs"] = (torch.zeros(m.numel() // BLOCK, dtype=F32, device=DEVICE) for _ in "mv")
+    else:
+        s["m8"], s["ms"] = encode_m(m)
+        s["v8"], s["vs"] = encode_v(v)
+    if kind == "decode":
+        s["m"], s["v"] = torch.zeros_like(m), torch.zeros_like(v)
+    if kind == "plan8":
+        dtype = F32 if case["fp32_grad"] else BF16
+        s["window"], s["step"] = case["window"], STEP
+        s["grads"] = [[gradients(gen, b[0], b[3], up(b[3]), dtype) for b in buckets] for _ in range(case["window"])]
+        s["p"] = torch.cat([weights(gen, b[3], up(b[3])) for b in buckets])
+        s["copy"] = torch.zeros(s["p"].numel(), dtype=BF16, device=DEVICE) if case["bf16"] else None
+        s["acc"] = torch.zeros_like(s["p"])
+        s["divisors"] = [torch.tensor(float(b[1]), device=DEVICE) for b in buckets]
+        s["lens"] = [(up(b[3]), b[2]) for b in buckets]
+        s["decayed"] = torch.cat([torch.full((up(b[3]),), b[2], device=DEVICE) for b in buckets])
+    s["wide"] = torch.tensor([64], dtype=torch.int16, device=DEVICE)
+    if own:
+        from gradient_reduction_optimizer_amd import binding as B
+        from gradient_reduction_optimizer_amd.buffers import Plan
+        specs = [dict(param_id=i, shape=(n,), placement=pl, shard_index=0 if pl == "shard" else -1, no_decay=not dec,
+                      fp32_grad=case.get("fp32_grad", False)) for i, (n, pl, dec) in enumerate(tensors_of(case))]
+        plan = Plan(specs, case.get("R", 1), 1 << 40)
+        assert plan.info["n_flat"] == m.numel() and plan.info["n_buckets"] == len(buckets)
+        room = torch.zeros(plan.info["workspace_bytes"] + 256, dtype=torch.uint8, device=DEVICE)
+        B.gro_plan_bind(plan.handle, (room.data_ptr() + 255) // 256 * 256, plan.info["workspace_bytes"],
+                        torch.cuda.current_stream().cuda_stream)
+        s["plan"], s["room"] = plan, room
+        s["state8"] = tuple(s[k].data_ptr() for k in ("m8", "v8", "ms", "vs"))
+    return s
+
+
+def in32(case, t):
+    """Whether a tensor's moments are held in 32 bits."""
+    return case["state"] == "32" or (case["state"] == "mixed" and t[0] < 4096)
+
+
+def prepare_group(case, gen):
+    """Tensors in one allocation for each kind of state, each from a multiple of 64 elements on, zeros between them."""
+    every = tensors_of(case)
+    s = {"kind": "group", "window": case["window"], "step": STEP, "parts": []}
+    dtype = F32 if case["fp32_grad"] else BF16
+    at = [None] * len(every)
+    for small in (True, False):
+        mine = [i for i, t in enumerate(every) if in32(case, t) == small]
+        if not mine:
+            continue
+        n = sum(up(every[i][0]) for i in mine)
+        real = torch.zeros(n, dtype=torch.bool, device=DEVICE)
+        decayed = torch.zeros(n, dtype=torch.bool, device=DEVICE)
+        off = 0
+        for i in mine:
+            at[i] = (len(s["parts"]), off)
+            real[off:off + every[i][0]] = True
+            decayed[off:off + every[i][0]] = every[i][2]
+            off += up(every[i][0])
+        q = {"g": gradients(gen, 1, n, n, dtype)[0] * real, "p": weights(gen, n, n) * real, "decayed": decayed,
+             "copy": torch.zeros(n, dtype=BF16, device=DEVICE) if case["bf16"] else None}
+        m, v = (x * real for x in moments(gen, n, n))
+        if small:
+            q["m"], q["v"] = m, v
+        else:
+            q["m8"], q["ms"] = encode_m(m)
+            q["v8"], q["vs"] = encode_v(v)
+        s["parts"].append(q)
+    s["wide"] = torch.tensor([64], dtype=torch.int16, device=DEVICE)
+    if own:
+        from gradient_reduction_optimizer_amd.buffers import TensorGroup
+        cut = lambda q, key, off, n: s["parts"][q][key][off:off + n]  # noqa: E731
+        masters, copies, states, s["grads"] = [], [], [], []
+        for (n, _, _), (q, off) in zip(every, at):
+            masters.append(cut(q, "p", off, n))
+            copies.append(cut(q, "copy", off, n) if case["bf16"] else None)
+            s["grads"].append(cut(q, "g", off, n))
+            if "m" in s["parts"][q]:
+                states.append((cut(q, "m", off, n), cut(q, "v", off, n)))
+            else:
+                b, nb = off // BLOCK, up(n) // BLOCK
+                states.append((cut(q, "m8", off, n), cut(q, "v8", off, n), cut(q, "ms", b, nb), cut(q, "vs", b, nb)))
+        s["group"] = TensorGroup(masters, state_bits=[32 if in32(case, t) else 8 for t in every],
+                                 no_decay=[not t[2] for t in every], grad_dtype=dtype, params_bf16=copies, states=states)
+    return s
+
+
+# -------------------------------------------------------------- plain form
+def encode_m(m):
+    """e4m3 codes and block scales of first moments; a block below 2^-100 is held as zeros."""
+    b = m.view(-1, BLOCK)
+    s = b.abs().amax(1)
+    s = torch.where(s < 2.0 ** -100, 0.0, s)
+    inv = torch.where(s > 0, 256.0 / s, 0.0)
+    return (b * inv[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).view(-1), s
+
+
+def encode_v(v):
+    """Codes and block scales of second moments: sqrt(v) / s rounded to 4 exponent and 4 mantissa bits."""
+    r = v.sqrt().view(-1, BLOCK)
+    s = r.amax(1)
+    inv = torch.where(s > 0, 1.0 / s, 0.0)
+    bits = ((r * inv[:, None]) * 2.0 ** -112).view(torch.int32)
+    code = (bits + 0x3FFFF + ((bits >> 19) & 1)) >> 19
+    code = torch.where(r > 0, code.clamp_min(1), 0)
+    return code.to(torch.uint8).view(-1), s
+
+
+def decode_m(m8, ms):
+    f = m8.view(torch.float8_e4m3fn).float() * (1 / 256)
+    return (f.view(-1, BLOCK) * ms[:, None]).view(-1)
+
+
+def decode_v(v8, vs, wide):
+    r = (fractions(v8, wide).float().view(-1, BLOCK) * vs[:, None]).view(-1)
+    return r * r
+
+
+def fractions(v8, wide):
+    """The values that second-moment codes stand for, as parts of their block's scale (exact in FP16)."""
+    return (v8 * wide).view(torch.float16)
+
+
+def scalars(step):
+    return {"step_size": LR / (1 - BETA1 ** step), "root": math.sqrt(1 - BETA2 ** step)}
+
+
+def clip(total):
+    """The clip coefficient of a gradient with this sum of squares."""
+    return (MAX_NORM / (total.sqrt() + 1e-6)).clamp_max(1.0).float()
+
+
+def squares(g):
+    return g.double().square().sum()
+
+
+def adamw(g, p, m, v, decayed, k):
+    m = m * BETA1 + g * (1 - BETA1)
+    v = v * BETA2 + (g * g) * (1 - BETA2)
+    d = v.sqrt() / k["root"] + EPS
+    p = torch.where(decayed, p * (1 - LR * DECAY), p) - (m / d) * k["step_size"]
+    return p, m, v
+
+
+def update(q, g, wide, k):
+    """One AdamW step on flat arrays, in place."""
+    if "m" in q:
+        p, m, v = adamw(g, q["p"], q["m"], q["v"], q["decayed"], k)
+        q["m"].copy_(m)
+        q["v"].copy_(v)
+    else:
+        p, m, v = adamw(g, q["p"], decode_m(q["m8"], q["ms"]), decode_v(q["v8"], q["vs"], wide), q["decayed"], k)
+        m8, ms = encode_m(m)
+        v8, vs = encode_v(v)
+        q["m8"].copy_(m8)
+        q["v8"].copy_(v8)
+        q["ms"].copy_(ms)
+        q["vs"].copy_(vs)
+    q["p"].copy_(p)
+    if q["copy"] is not None:
+        q["copy"].copy_(p)
+
+
+def held(q, wide):
+    """What a set holds after a step: 8-bit moments as the parts of the scale that their codes stand for."""
+    got = {"p": q["p"], "copy": q["copy"]}
+    if "m" in q:
+        got.update(m=q["m"], v=q["v"])
+    else:
+        got.update(m=q["m8"].view(torch.float8_e4m3fn), v=fractions(q["v8"], wide), m_scale=q["ms"], v_scale=q["vs"])
+    return got
+
+
+def run(s):
+    return {"plan8": run_plan8, "encode": run_encode, "decode": run_decode, "group": run_group}[s["kind"]](s)
+
+
+def run_encode(s):
+    if own:
+        from gradient_reduction_optimizer_amd import binding as B
+        B.gro_state8_encode(s["plan"].handle, s["m"].data_ptr(), s["v"].data_ptr(), s["state8"],
+                            torch.cuda.current_stream().cuda_stream)
+        m8, v8, ms, vs = s["m8"], s["v8"], s["ms"], s["vs"]
+    else:
+        m8, ms = encode_m(s["m"])
+        v8, vs = encode_v(s["v"])
+    return {"m": m8.view(torch.float8_e4m3fn), "v": fractions(v8, s["wide"]), "m_scale": ms, "v_scale": vs}
+
+
+def run_decode(s):
+    if own:
+        from gradient_reduction_optimizer_amd import binding as B
+        B.gro_state8_decode(s["plan"].handle, s["state8"], s["m"].data_ptr(), s["v"].data_ptr(),
+                            torch.cuda.current_stream().cuda_stream)
+        return {"m": s["m"], "v": s["v"]}
+    return {"m": decode_m(s["m8"], s["ms"]), "v": decode_v(s["v8"], s["vs"], s["wide"])}
+
+
+def run_plan8(s):
+    s["step"] += 1
+    if own:
+        from gradient_reduction_optimizer_amd import binding as B
+        stream, h, acc, n = torch.cuda.current_stream().cuda_stream, s["plan"].handle, s["acc"].data_ptr(), s["window"]
+        B.gro_accumulate_window(h, 0, len(s["lens"]), [b.data_ptr() for micro in s["grads"] for b in micro], n, acc, stream)
+        B.gro_reduce_norm(h, acc, n, stream)
+        B.gro_clip_adamw8(h, acc, n, MAX_NORM, dict(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY),
+                          s["step"], s["p"].data_ptr(), s["state8"],
+                          0 if s["copy"] is None else s["copy"].data_ptr(), stream)
+        return {"acc": s["acc"], **held(s, s["wide"])}
+    reduced = [torch.cat([b.float().sum(0) / d for b, d in zip(micro, s["divisors"])]) for micro in s["grads"]]
+    acc = functools.reduce(torch.add, reduced)
+    g = acc / float(s["window"])
+    update(s, g * clip(squares(g)), s["wide"], scalars(s["step"]))
+    return {"acc": acc, **held(s, s["wide"])}
+
+
+def run_group(s):
+    s["step"] += 1
+    if own:
+        s["group"].norm(s["grads"], s["window"])
+        s["group"].clip_adamw(MAX_NORM, dict(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY), s["step"])
+    else:
+        grads = [q["g"].float() / float(s["window"]) for q in s["parts"]]
+        coef = clip(functools.reduce(torch.add, [squares(g) for g in grads]))
+        k = scalars(s["step"])
+        for q, g in zip(s["parts"], grads):
+            update(q, g * coef, s["wide"], k)
+    return [held(q, s["wide"]) for q in s["parts"]]
+
+
+# --------------------------------------------------- the definition, 64 bits
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["kind"] == "encode":
+        return exact_codes(s["m"].to(F64), s["v"].to(F64))
+    if case["kind"] == "decode":
+        m, v = exact_moments(s)
+        return {"m": m, "v": v}
+    if case["kind"] == "plan8":
+        acc = 0
+        for micro in s["grads"]:
+            flat = []
+            for b, (slots, divisor, _, _) in zip(micro, buckets_of(case)):
+                total = b[0].to(F64)
+                for r in range(1, slots):
+                    total = total + b[r].to(F64)
+                flat.append(total / divisor)
+            acc = acc + torch.cat(flat)
+        g = acc / case["window"]
+        norm = float(torch.linalg.vector_norm(g))
+        return {"acc": acc, **exact_step(s, g, norm)}
+    grads = [q["g"].to(F64) / case["window"] for q in s["parts"]]
+    norm = math.sqrt(sum(float(torch.linalg.vector_norm(g)) ** 2 for g in grads))
+    return [exact_step(q, g, norm) for q, g in zip(s["parts"], grads)]
+
+
+def exact_step(q, g, norm):
+    t = STEP + 1
+    g = g * min(1.0, MAX_NORM / (norm + 1e-6))
+    m, v = (q["m"].to(F64), q["v"].to(F64)) if "m" in q else exact_moments(q)
+    m = BETA1 * m + (1 - BETA1) * g
+    v = BETA2 * v + (1 - BETA2) * g ** 2
+    p = q["p"].to(F64) * (1 - LR * DECAY * q["decayed"].to(F64))
+    p = p - LR * (m / (1 - BETA1 ** t)) / ((v / (1 - BETA2 ** t)) ** 0.5 + EPS)
+    got = {"p": p, "copy": None if q["copy"] is None else p}
+    got.update({"m": m, "v": v} if "m" in q else exact_codes(m, v))
+    return got
+
+
+def exact_moments(q):
+    """m and v from 8-bit codes, by the bits' meaning."""
+    c = q["m8"].to(torch.int64)
+    e, f = (c >> 3) & 15, (c & 7).to(F64)
+    size = torch.where(e == 0, f * 2.0 ** -9, torch.ldexp(1 + f / 8, e - 7))
+    m = torch.where(c >= 128, -size, size) / 256 * q["ms"].to(F64).repeat_interleave(BLOCK)
+    c = q["v8"].to(torch.int64)
+    e, f = c >> 4, (c & 15).to(F64)
+    r = torch.where(e == 0, f * 2.0 ** -18, torch.ldexp(1 + f / 16, e - 15)) * q["vs"].to(F64).repeat_interleave(BLOCK)
+    return m, r * r
+
+
+def nearest(y, digits, lowest):
+    """y >= 0 to the nearest float of so many mantissa bits, ties to even, exponents from `lowest` on."""
+    e = (torch.frexp(y).exponent - 1).clamp_min(lowest)
+    unit = torch.ldexp(torch.ones_like(y), e - digits)
+    return torch.round(y / unit) * unit
+
+
+def exact_codes(m, v):
+    b = m.view(-1, BLOCK)
+    s = b.abs().amax(1)
+    s = torch.where(s < 2.0 ** -100, torch.zeros_like(s), s)
+    y = 256 * b.abs() / torch.where(s > 0, s, torch.ones_like(s))[:, None]
+    f = (torch.sign(b) * nearest(y, 3, -6)).view(-1)
+    r = torch.sqrt(v).view(-1, BLOCK)
+    t = r.amax(1)
+    y = r / torch.where(t > 0, t, torch.ones_like(t))[:, None]
+    w = nearest(y, 4, -14)
+    w = torch.where(r > 0, w.clamp_min(2.0 ** -18), w).view(-1)
+    return {"m": f, "v": w, "m_scale": s, "v_scale": t}
