@@ -204,7 +204,7 @@ def prepare_plan(case, gen):
         B.gro_plan_bind(plan.handle, (room.data_ptr() + 255) // 256 * 256, plan.info["workspace_bytes"],
                         torch.cuda.current_stream().cuda_stream)
         s["plan"], s["room"] = plan, room
-        s["state8"] = tuple(s[k].data_ptr() for k in ("m8", "v8", "ms", "vs"))
+        s["coded"] = tuple(s[k].data_ptr() for k in ("m8", "v8", "ms", "vs"))
     return s
 
 
@@ -353,7 +353,7 @@ def run(s):
 def run_encode(s):
     if own:
         from gradient_reduction_optimizer_amd import binding as B
-        B.gro_state8_encode(s["plan"].handle, s["m"].data_ptr(), s["v"].data_ptr(), s["state8"],
+        B.gro_moments_encode(s["plan"].handle, s["m"].data_ptr(), s["v"].data_ptr(), s["coded"],
                             torch.cuda.current_stream().cuda_stream)
         m8, v8, ms, vs = s["m8"], s["v8"], s["ms"], s["vs"]
     else:
@@ -365,7 +365,7 @@ def run_encode(s):
 def run_decode(s):
     if own:
         from gradient_reduction_optimizer_amd import binding as B
-        B.gro_state8_decode(s["plan"].handle, s["state8"], s["m"].data_ptr(), s["v"].data_ptr(),
+        B.gro_moments_decode(s["plan"].handle, s["coded"], s["m"].data_ptr(), s["v"].data_ptr(),
                             torch.cuda.current_stream().cuda_stream)
         return {"m": s["m"], "v": s["v"]}
     return {"m": decode_m(s["m8"], s["ms"]), "v": decode_v(s["v8"], s["vs"], s["wide"])}
@@ -378,8 +378,8 @@ def run_plan8(s):
         stream, h, acc, n = torch.cuda.current_stream().cuda_stream, s["plan"].handle, s["acc"].data_ptr(), s["window"]
         B.gro_accumulate_window(h, 0, len(s["lens"]), [b.data_ptr() for micro in s["grads"] for b in micro], n, acc, stream)
         B.gro_reduce_norm(h, acc, n, stream)
-        B.gro_clip_adamw8(h, acc, n, MAX_NORM, dict(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY),
-                          s["step"], s["p"].data_ptr(), s["state8"],
+        B.gro_clip_adamw_coded(h, acc, n, MAX_NORM, dict(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY),
+                          s["step"], s["p"].data_ptr(), s["coded"],
                           0 if s["copy"] is None else s["copy"].data_ptr(), stream)
         return {"acc": s["acc"], **held(s, s["wide"])}
     reduced = [torch.cat([b.float().sum(0) / d for b, d in zip(micro, s["divisors"])]) for micro in s["grads"]]
