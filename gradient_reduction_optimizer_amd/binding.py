@@ -27,18 +27,21 @@ ERROR_NAMES = {GRO_E_INVALID: "invalid", GRO_E_PLACEMENT: "placement",
 GRO_REPLICATE, GRO_PARTIAL, GRO_SHARD, GRO_REDUCED = 0, 1, 2, 3
 PLACEMENT_CODES = {"replicate": GRO_REPLICATE, "partial": GRO_PARTIAL,
                    "shard": GRO_SHARD, "reduced": GRO_REDUCED}
-GRO_NO_DECAY, GRO_FROZEN, GRO_FP32_GRAD = 1, 2, 4
+GRO_NO_DECAY, GRO_FROZEN, GRO_FP32_GRAD, GRO_CODED_MOMENTS = 1, 2, 4, 8
 GRO_GRAD_BF16, GRO_GRAD_FP32 = 0, 1
 GRO_OWNER_MEAN, GRO_OWNER_SUM, GRO_OWNER_LOCAL_SHARD, GRO_OWNER_LOCAL_REDUCED, GRO_OWNER_EXCLUDED = range(5)
 OWNER_NAMES = ("mean", "sum", "local_shard", "local_reduced", "excluded")
 GRO_MAX_NDIM = 8
 GRO_STATIC_WORKSPACE_BYTES = 16777216
+GRO_CODED_BLOCK = 64
 
 EXPORTS = ("gro_plan_create", "gro_plan_destroy", "gro_plan_get_info", "gro_plan_tensor",
            "gro_plan_bucket", "gro_plan_bind", "gro_plan_bind_static", "gro_accumulate", "gro_accumulate_window",
            "gro_accumulate_microbatches",
            "gro_reduce_norm", "gro_plan_get_norm", "gro_clip_adamw", "gro_init_uniform",
-           "gro_last_error")
+           "gro_clip_adamw_coded", "gro_moments_encode", "gro_moments_decode", "gro_group_create",
+           "gro_group_destroy", "gro_group_get_info", "gro_group_bind", "gro_group_norm", "gro_group_clip_adamw",
+           "gro_group_get_norm", "gro_last_error")
 
 
 class gro_tensor_desc(ctypes.Structure):
@@ -72,6 +75,25 @@ class gro_bucket_info(ctypes.Structure):
 class gro_adamw_hparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class gro_coded_moments(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class gro_group_desc(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class gro_group_tensor(ctypes.Structure):
+    _fields_ = [("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p)]
+
+
+class gro_group_info(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("chunk_elems", ctypes.c_int32), ("n_chunks", ctypes.c_int64),
+                ("n_elems", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
 
 
 class GroError(RuntimeError):
@@ -121,10 +143,22 @@ def load() -> ctypes.CDLL:
     L.gro_plan_get_norm.argtypes = [P, ctypes.POINTER(D), ctypes.POINTER(D), ctypes.POINTER(I32)]
     L.gro_clip_adamw.argtypes = [P, P, I32, D, ctypes.POINTER(gro_adamw_hparams), I64, P, P, P, P, P]
     L.gro_init_uniform.argtypes = [P, ctypes.c_uint64, ctypes.POINTER(D), ctypes.POINTER(D), P, P, P]
+    L.gro_clip_adamw_coded.argtypes = [P, P, I32, D, ctypes.POINTER(gro_adamw_hparams), I64, P,
+                                       ctypes.POINTER(gro_coded_moments), P, P]
+    L.gro_moments_encode.argtypes = [P, P, P, ctypes.POINTER(gro_coded_moments), P]
+    L.gro_moments_decode.argtypes = [P, ctypes.POINTER(gro_coded_moments), P, P, P]
+    L.gro_group_create.argtypes = [ctypes.POINTER(gro_group_desc), I32, ctypes.POINTER(P)]
+    L.gro_group_destroy.argtypes = [P]
+    L.gro_group_destroy.restype = None
+    L.gro_group_get_info.argtypes = [P, ctypes.POINTER(gro_group_info)]
+    L.gro_group_bind.argtypes = [P, ctypes.POINTER(gro_group_tensor), P, U64, P]
+    L.gro_group_norm.argtypes = [P, ctypes.POINTER(P), I32, P]
+    L.gro_group_clip_adamw.argtypes = [P, D, ctypes.POINTER(gro_adamw_hparams), I64, P]
+    L.gro_group_get_norm.argtypes = [P, ctypes.POINTER(D), ctypes.POINTER(D), ctypes.POINTER(I32)]
     L.gro_last_error.argtypes = []
     L.gro_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
-        if name not in ("gro_plan_destroy", "gro_last_error"):
+        if name not in ("gro_plan_destroy", "gro_group_destroy", "gro_last_error"):
             getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -267,10 +301,14 @@ def gro_plan_get_norm(plan: int):
     return n.value, sq.value, bool(f.value)
 
 
+def _hparams(hp: dict) -> gro_adamw_hparams:
+    return gro_adamw_hparams(float(hp["lr"]), float(hp["beta1"]), float(hp["beta2"]), float(hp["eps"]),
+                             float(hp["weight_decay"]))
+
+
 def gro_clip_adamw(plan: int, d_acc: int, window_size: int, max_norm: float, hp: dict, step: int,
                    d_master: int, d_m: int, d_v: int, d_param_bf16: int = 0, stream: int = 0) -> None:
-    h = gro_adamw_hparams(float(hp["lr"]), float(hp["beta1"]), float(hp["beta2"]), float(hp["eps"]),
-                          float(hp["weight_decay"]))
+    h = _hparams(hp)
     _check(load().gro_clip_adamw(ctypes.c_void_p(plan), ctypes.c_void_p(d_acc), int(window_size),
                                  float(max_norm), ctypes.byref(h), int(step), ctypes.c_void_p(d_master),
                                  ctypes.c_void_p(d_m), ctypes.c_void_p(d_v),
@@ -291,3 +329,93 @@ def gro_init_uniform(plan: int, seed: int, bounds: Sequence[float], offsets: Opt
     _check(load().gro_init_uniform(ctypes.c_void_p(plan), ctypes.c_uint64(int(seed) & ((1 << 64) - 1)), b, o,
                                    ctypes.c_void_p(d_master), ctypes.c_void_p(d_param_bf16 or 0),
                                    ctypes.c_void_p(stream)))
+
+
+def _coded(moments: Sequence[int]) -> gro_coded_moments:
+    if len(moments) != 4:
+        raise ValueError(f"8-bit moments are four pointers (m, v, m_scale, v_scale), got {len(moments)}")
+    return gro_coded_moments(*[int(p) for p in moments])
+
+
+def gro_clip_adamw_coded(plan: int, d_acc: int, window_size: int, max_norm: float, hp: dict, step: int,
+                         d_master: int, moments: Sequence[int], d_param_bf16: int = 0, stream: int = 0) -> None:
+    """moments: the pointers (m, v, m_scale, v_scale) of the 8-bit moments."""
+    h, c = _hparams(hp), _coded(moments)
+    _check(load().gro_clip_adamw_coded(ctypes.c_void_p(plan), ctypes.c_void_p(d_acc), int(window_size),
+                                       float(max_norm), ctypes.byref(h), int(step), ctypes.c_void_p(d_master),
+                                       ctypes.byref(c), ctypes.c_void_p(d_param_bf16 or 0), ctypes.c_void_p(stream)))
+
+
+def gro_moments_encode(plan: int, d_m: int, d_v: int, moments: Sequence[int], stream: int = 0) -> None:
+    """FP32 moments of a plan to 8-bit ones (pointers m, v, m_scale, v_scale)."""
+    c = _coded(moments)
+    _check(load().gro_moments_encode(ctypes.c_void_p(plan), ctypes.c_void_p(d_m), ctypes.c_void_p(d_v),
+                                     ctypes.byref(c), ctypes.c_void_p(stream)))
+
+
+def gro_moments_decode(plan: int, moments: Sequence[int], d_m: int, d_v: int, stream: int = 0) -> None:
+    """8-bit moments of a plan (pointers m, v, m_scale, v_scale) to FP32 ones."""
+    c = _coded(moments)
+    _check(load().gro_moments_decode(ctypes.c_void_p(plan), ctypes.byref(c), ctypes.c_void_p(d_m),
+                                     ctypes.c_void_p(d_v), ctypes.c_void_p(stream)))
+
+
+def gro_group_create(tensors: Sequence) -> int:
+    """``tensors``: objects or dicts with numel and optional no_decay /
+    fp32_grad / coded_moments.  Returns the group handle."""
+    n = len(tensors)
+    descs = (gro_group_desc * max(n, 1))()
+    for i, t in enumerate(tensors):
+        flags = (GRO_NO_DECAY if _attr(t, "no_decay", False) else 0) | \
+                (GRO_FP32_GRAD if _attr(t, "fp32_grad", False) else 0) | \
+                (GRO_CODED_MOMENTS if _attr(t, "coded_moments", False) else 0) | int(_attr(t, "flags", 0) or 0)
+        descs[i] = gro_group_desc(int(_attr(t, "numel")), flags, 0)
+    out = ctypes.c_void_p()
+    _check(load().gro_group_create(descs if n else None, n, ctypes.byref(out)))
+    return int(out.value)
+
+
+def gro_group_destroy(group: int) -> None:
+    if group:
+        load().gro_group_destroy(ctypes.c_void_p(group))
+
+
+def gro_group_get_info(group: int) -> dict:
+    info = gro_group_info()
+    _check(load().gro_group_get_info(ctypes.c_void_p(group), ctypes.byref(info)))
+    return _struct_dict(info)
+
+
+def gro_group_bind(group: int, tensors: Sequence[Sequence[int]], d_workspace: int, nbytes: int,
+                   stream: int = 0) -> None:
+    """tensors: per tensor the pointers (master, m, v, m_scale, v_scale,
+    param_bf16), 0 for those it has not."""
+    n = gro_group_get_info(group)["n_tensors"]
+    if len(tensors) != n:
+        raise ValueError(f"gro_group_bind: {len(tensors)} tensors given, the group has {n}")
+    rows = (gro_group_tensor * max(n, 1))()
+    for i, t in enumerate(tensors):
+        rows[i] = gro_group_tensor(*[int(p) for p in t])
+    _check(load().gro_group_bind(ctypes.c_void_p(group), rows, ctypes.c_void_p(d_workspace), int(nbytes),
+                                 ctypes.c_void_p(stream)))
+
+
+def gro_group_norm(group: int, d_grads: Sequence[int], window_size: int = 1, stream: int = 0) -> None:
+    """d_grads: one pointer per tensor, 0 for a tensor that has no gradient in
+    this step."""
+    n = gro_group_get_info(group)["n_tensors"]
+    ptrs = _pointer_array(d_grads, n, "gro_group_norm")
+    _check(load().gro_group_norm(ctypes.c_void_p(group), ptrs, int(window_size), ctypes.c_void_p(stream)))
+
+
+def gro_group_clip_adamw(group: int, max_norm: float, hp: dict, step: int, stream: int = 0) -> None:
+    h = _hparams(hp)
+    _check(load().gro_group_clip_adamw(ctypes.c_void_p(group), float(max_norm), ctypes.byref(h), int(step),
+                                       ctypes.c_void_p(stream)))
+
+
+def gro_group_get_norm(group: int):
+    """Returns (norm, norm_sq, finite)."""
+    n, sq, f = ctypes.c_double(), ctypes.c_double(), ctypes.c_int32()
+    _check(load().gro_group_get_norm(ctypes.c_void_p(group), ctypes.byref(n), ctypes.byref(sq), ctypes.byref(f)))
+    return n.value, sq.value, bool(f.value)

@@ -6,7 +6,7 @@ bytes (the kernels in libgro.so do the work).
 """
 from __future__ import annotations
 
-from typing import Dict, List, Sequence, Tuple
+from typing import List, Optional, Sequence, Tuple
 
 from . import binding as B
 
@@ -54,10 +54,13 @@ class DeviceState:
     """FP32 accumulator / master / m / v, the BF16 parameter copy and the
     workspace for one plan, allocated with torch on ``device`` and bound.
     With ``static_workspace`` no workspace is allocated: the plan is bound
-    to the library's own per-GPU workspace (gro_plan_bind_static)."""
+    to the library's own per-GPU workspace (gro_plan_bind_static).  With
+    ``coded_moments`` the moments are held in 8 bits: ``m`` and ``v`` are
+    code bytes, ``m_scale`` and ``v_scale`` the blocks' scales, and ``coded``
+    their four pointers, for gro_clip_adamw_coded."""
 
     def __init__(self, plan: Plan, device="cuda", with_bf16: bool = True, stream=None,
-                 static_workspace: bool = False):
+                 static_workspace: bool = False, coded_moments: bool = False):
         import torch
         self.plan = plan
         self.device = torch.device(device)
@@ -65,8 +68,16 @@ class DeviceState:
         f32 = dict(dtype=torch.float32, device=self.device)
         self.acc = torch.zeros(n, **f32)
         self.master = torch.zeros(n, **f32)
-        self.m = torch.zeros(n, **f32)
-        self.v = torch.zeros(n, **f32)
+        self.coded = None
+        if coded_moments:
+            self.m = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self.v = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self.m_scale = torch.zeros(-(-n // B.GRO_CODED_BLOCK), **f32)
+            self.v_scale = torch.zeros(-(-n // B.GRO_CODED_BLOCK), **f32)
+            self.coded = tuple(t.data_ptr() for t in (self.m, self.v, self.m_scale, self.v_scale))
+        else:
+            self.m = torch.zeros(n, **f32)
+            self.v = torch.zeros(n, **f32)
         self.p_bf16 = torch.zeros(n, dtype=torch.bfloat16, device=self.device) if with_bf16 else None
         self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
         if static_workspace:
@@ -79,6 +90,32 @@ class DeviceState:
         self.ws_ptr = (base + 255) // 256 * 256
         self.ws_bytes = nbytes
         B.gro_plan_bind(plan.handle, self.ws_ptr, nbytes, self.stream.cuda_stream)
+
+    def moments(self):
+        """The moments as flat FP32 arrays (m, v): the state's own, or, held in
+        8 bits, decoded ones (zeros between buckets)."""
+        import torch
+        if self.coded is None:
+            return self.m, self.v
+        m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
+        B.gro_moments_decode(self.plan.handle, self.coded, m.data_ptr(), v.data_ptr(),
+                             torch.cuda.current_stream(self.device).cuda_stream)
+        return m, v
+
+    def set_moments(self, m, v) -> None:
+        """Take flat FP32 moments over, encoded if the state holds 8 bits."""
+        import torch
+        for name, t in (("m", m), ("v", v)):
+            if t.dtype != torch.float32 or t.shape != self.master.shape:
+                raise ValueError(f"{name}: flat FP32 moments have shape {tuple(self.master.shape)}, "
+                                 f"got {t.dtype} {tuple(t.shape)}")
+        if self.coded is None:
+            self.m.copy_(m)
+            self.v.copy_(v)
+            return
+        m, v = m.to(self.device).contiguous(), v.to(self.device).contiguous()
+        B.gro_moments_encode(self.plan.handle, m.data_ptr(), v.data_ptr(), self.coded,
+                             torch.cuda.current_stream(self.device).cuda_stream)
 
     def grad_buffers(self) -> List:
         """One [slots, slot_stride] buffer per bucket (zeros), BF16 or FP32
@@ -101,3 +138,120 @@ class DeviceState:
         t = self.plan.tensors[i]
         off = t["flat_offset"]
         return arr[off:off + t["numel"]] if off >= 0 else arr[:0]
+
+
+def _check_array(what: str, t, dtype, numel: int, device) -> None:
+    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of {numel} elements on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+class TensorGroup:
+    """Many FP32 master tensors stepped at once where they lie, bound to a
+    workspace of its own: gro_group_norm and gro_group_clip_adamw.
+
+    ``masters``: contiguous FP32 tensors of one GPU.  Per tensor, as one value
+    for all or a list: ``state_bits`` (32 or 8: how the moments are held),
+    ``no_decay``, ``grad_dtype`` (torch.bfloat16 or torch.float32).
+    ``params_bf16``: BF16 copies to update along, None for a tensor without.
+    ``states``: per tensor (m, v) or, in 8 bits, (m, v, m_scale, v_scale);
+    zeros are allocated when it is not given.  The tensors stay the caller's;
+    the group keeps references to them."""
+
+    def __init__(self, masters: Sequence, state_bits=32, no_decay=False, grad_dtype=None,
+                 params_bf16: Optional[Sequence] = None, states: Optional[Sequence] = None, stream=None):
+        import torch
+        self.handle = 0
+        n = len(masters)
+        per_tensor = lambda x: list(x) if isinstance(x, (list, tuple)) else [x] * n  # noqa: E731
+        bits = per_tensor(state_bits)
+        no_decay = per_tensor(no_decay)
+        grad_dtype = per_tensor(torch.bfloat16 if grad_dtype is None else grad_dtype)
+        copies = [None] * n if params_bf16 is None else list(params_bf16)
+        for what, x in (("state_bits", bits), ("no_decay", no_decay), ("grad_dtype", grad_dtype),
+                        ("params_bf16", copies), ("states", bits if states is None else states)):
+            if len(x) != n:
+                raise ValueError(f"{what}: {len(x)} entries for {n} tensors")
+        if any(b not in (8, 32) for b in bits):
+            raise ValueError("state_bits is 8 or 32")
+        if any(d not in (torch.bfloat16, torch.float32) for d in grad_dtype):
+            raise ValueError("grad_dtype is torch.bfloat16 or torch.float32")
+        self.device = masters[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        if self.device.type != "cuda":
+            raise ValueError(f"a group's tensors are on a GPU, got {self.device}")
+        self.masters, self.copies, self.bits, self.grad_dtype = list(masters), copies, bits, grad_dtype
+        self.states = []
+        rows = []
+        for i, p in enumerate(masters):
+            k = p.numel()
+            _check_array(f"master {i}", p, torch.float32, k, self.device)
+            if copies[i] is not None:
+                _check_array(f"params_bf16 {i}", copies[i], torch.bfloat16, k, self.device)
+            kinds = [torch.float32] * 2 if bits[i] == 32 else [torch.uint8] * 2 + [torch.float32] * 2
+            sizes = [k, k, -(-k // B.GRO_CODED_BLOCK), -(-k // B.GRO_CODED_BLOCK)][:len(kinds)]
+            if states is None:
+                st = tuple(torch.zeros(s, dtype=d, device=self.device) for s, d in zip(sizes, kinds))
+            else:
+                st = tuple(states[i])
+                if len(st) != len(kinds):
+                    raise ValueError(f"states {i}: {len(kinds)} tensors are needed, got {len(st)}")
+                for t, s, d in zip(st, sizes, kinds):
+                    _check_array(f"states {i}", t, d, s, self.device)
+            self.states.append(st)
+            ptrs = [t.data_ptr() for t in st] + [0] * (4 - len(st))
+            rows.append([p.data_ptr(), *ptrs, 0 if copies[i] is None else copies[i].data_ptr()])
+        self.handle = B.gro_group_create([dict(numel=p.numel(), no_decay=bool(nd), coded_moments=b == 8,
+                                               fp32_grad=gd == torch.float32)
+                                          for p, nd, b, gd in zip(masters, no_decay, bits, grad_dtype)])
+        self.info = B.gro_group_get_info(self.handle)
+        nbytes = int(self.info["workspace_bytes"])
+        self.workspace = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(self.device):
+            B.gro_group_bind(self.handle, rows, (self.workspace.data_ptr() + 255) // 256 * 256, nbytes,
+                             self._stream(stream))
+        self._grads = None
+
+    def _stream(self, stream) -> int:
+        import torch
+        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+
+    def close(self) -> None:
+        if self.handle:
+            B.gro_group_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def norm(self, grads: Sequence, window_size: int = 1, stream=None) -> None:
+        """gro_group_norm of ``grads`` (one per tensor, None for a tensor left
+        out of this step) on ``stream``, by default the current one."""
+        import torch
+        if len(grads) != len(self.masters):
+            raise ValueError(f"{len(grads)} gradients for {len(self.masters)} tensors")
+        ptrs = []
+        for i, g in enumerate(grads):
+            if g is None:
+                ptrs.append(0)
+                continue
+            _check_array(f"gradient {i}", g, self.grad_dtype[i], self.masters[i].numel(), self.device)
+            ptrs.append(g.data_ptr())
+        with torch.cuda.device(self.device):
+            B.gro_group_norm(self.handle, ptrs, window_size, self._stream(stream))
+        self._grads = list(grads)  # in place until clip_adamw has been enqueued
+
+    def clip_adamw(self, max_norm: float, hp: dict, step: int, stream=None) -> None:
+        """gro_group_clip_adamw of the gradients given to ``norm``."""
+        import torch
+        with torch.cuda.device(self.device):
+            B.gro_group_clip_adamw(self.handle, max_norm, hp, step, self._stream(stream))
+        self._grads = None
+
+    def get_norm(self):
+        """(norm, norm_sq, finite) of the last ``norm``; waits for its stream."""
+        import torch
+        with torch.cuda.device(self.device):
+            return B.gro_group_get_norm(self.handle)

@@ -27,6 +27,8 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 ARCH = "gfx950"
 
+HIP_SOURCES = ("kernels", "moments", "group", "abi", "group_abi")
+
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-ffp-contract=off", "-Wall", f"-I{INCLUDE}", f"-I{CSRC}"]
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
@@ -47,7 +49,7 @@ def build(verbose: bool = False) -> str:
     o = os.path.join(BUILD, "plan.o")
     _run(["g++", *COMMON, "-c", os.path.join(CSRC, "plan.cpp"), "-o", o], verbose)
     objs.append(o)
-    for name in ("kernels", "abi"):
+    for name in HIP_SOURCES:
         o = os.path.join(BUILD, f"{name}.o")
         _run([HIPCC, *COMMON, *HIP_FLAGS, "-c", os.path.join(CSRC, f"{name}.hip"), "-o", o], verbose)
         objs.append(o)
@@ -82,7 +84,7 @@ def build_variant(name: str, defines, verbose: bool = False) -> str:
     o = os.path.join(VARIANTS, f"{name}_plan.o")
     _run(["g++", *COMMON, *dflags, "-c", os.path.join(CSRC, "plan.cpp"), "-o", o], verbose)
     objs.append(o)
-    for src in ("kernels", "abi"):
+    for src in HIP_SOURCES:
         o = os.path.join(VARIANTS, f"{name}_{src}.o")
         _run([HIPCC, *COMMON, *HIP_FLAGS, *dflags, "-c", os.path.join(CSRC, f"{src}.hip"), "-o", o], verbose)
         objs.append(o)

@@ -28,6 +28,12 @@ already-reduced, whose state is the whole parameter's).
 
 This is host plumbing around the plan's layout (torch copies), not part of
 the per-step path.  The arrays may live on any torch device.
+
+Moments held in 8 bits are saved as the FP32 values they stand for
+(save_device_state, load_device_state), because their blocks run across
+parameters and so depend on the layout.  Restored into the same layout they
+get the very same codes again; into another layout they are rounded once more,
+by other blocks' scales.
 """
 from __future__ import annotations
 
@@ -134,3 +140,20 @@ def load_state(plan, master, m, v, directory: str) -> int:
         for name, arr in (("master", master), ("m", m), ("v", v)):
             _slice(arr, row).copy_(state[f"{name}/{pid}"])
     return int(meta["step"])
+
+
+def save_device_state(st, step: int, directory: str) -> None:
+    """save_state of a buffers.DeviceState, with moments of 32 or 8 bits."""
+    m, v = st.moments()
+    save_state(st.plan, st.master, m, v, step, directory)
+
+
+def load_device_state(st, directory: str) -> int:
+    """load_state into a buffers.DeviceState, with moments of 32 or 8 bits;
+    returns the step."""
+    if st.coded is None:
+        return load_state(st.plan, st.master, st.m, st.v, directory)
+    m, v = st.moments()
+    step = load_state(st.plan, st.master, m, v, directory)
+    st.set_moments(m, v)
+    return step

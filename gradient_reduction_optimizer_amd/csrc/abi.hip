@@ -15,9 +15,11 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -31,12 +33,6 @@ using namespace gro;
 static __device__ __align__(256) unsigned char scratch[GRO_STATIC_WORKSPACE_BYTES];
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int hip_fail(hipError_t e, const char* what) {
-  return set_error(GRO_E_HIP, "%s: %s", what, hipGetErrorString(e));
-}
 
 // Device address of `scratch` on each device, looked up the first time a
 // plan is bound to it on that device (with that device current).
@@ -526,35 +522,79 @@ extern "C" int gro_plan_get_norm(gro_plan* p, double* norm, double* norm_sq, int
   return GRO_OK;
 }
 
+namespace {
+
+// What clip + AdamW needs of the window, whichever way the moments are held.
+// Any bucket at all: the accumulator of this window; always: its norm.
+int check_step_state(const gro_plan* p, const float* d_acc, int32_t window_size) {
+  if (!p->buckets.empty() && d_acc != p->acc_ptr)
+    return set_error(GRO_E_STATE, "d_acc is not the accumulator of this window");
+  if (!p->norm_done || p->norm_window != window_size)
+    return set_error(GRO_E_STATE, "gro_reduce_norm of this window (size %d) has not run", window_size);
+  return GRO_OK;
+}
+
+Range flat_range(const gro_plan* p, const void* a, uint64_t elem_bytes) {
+  return Range{reinterpret_cast<uintptr_t>(a), a ? uint64_t(p->n_flat) * elem_bytes : 0};
+}
+
+// The 8-bit moments' pointers, and that they overlap neither each other nor
+// the call's other (at most four) arrays.
+int check_coded(const gro_plan* p, const gro_coded_moments* c, std::initializer_list<Range> others) {
+  if (c == nullptr) return set_error(GRO_E_INVALID, "moments is NULL");
+  if (p->buckets.empty()) return GRO_OK;
+  const void* all[4] = {c->m, c->v, c->m_scale, c->v_scale};
+  for (const void* a : all)
+    if (a == nullptr || !aligned16(a))
+      return set_error(GRO_E_INVALID, "8-bit moment pointers must be non-NULL and 16-byte aligned");
+  const uint64_t n = uint64_t(p->n_flat), scales = n / kCodedBlock * sizeof(float);
+  Range r[8];
+  size_t k = 0;
+  for (int i = 0; i < 4; ++i) r[k++] = Range{reinterpret_cast<uintptr_t>(all[i]), i < 2 ? n : scales};
+  for (const Range& o : others) r[k++] = o;
+  if (first_overlap(r, k) >= 0) return set_error(GRO_E_INVALID, "arrays of the call overlap");
+  return GRO_OK;
+}
+
+int run_moments(gro_plan* p, const float* d_m, const float* d_v, const gro_coded_moments* moments, bool encode,
+                void* stream) {
+  int rc = check_bound(p);
+  if (rc != GRO_OK) return rc;
+  if (!p->buckets.empty() && (d_m == nullptr || !aligned16(d_m) || d_v == nullptr || !aligned16(d_v)))
+    return set_error(GRO_E_INVALID, "moment pointers must be non-NULL and 16-byte aligned");
+  rc = check_coded(p, moments, {flat_range(p, d_m, 4), flat_range(p, d_v, 4)});
+  if (rc != GRO_OK) return rc;
+  MomentsLaunch a;
+  a.chunks = dev_chunks(p);
+  a.n_chunks = int64_t(p->chunks.size());
+  a.m = const_cast<float*>(d_m);
+  a.v = const_cast<float*>(d_v);
+  a.moments = *moments;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = encode ? launch_moments_encode(a, s) : launch_moments_decode(a, s);
+  if (e != hipSuccess) return hip_fail(e, encode ? "moments encode launch" : "moments decode launch");
+  return GRO_OK;
+}
+
+}  // namespace
+
 extern "C" int gro_clip_adamw(gro_plan* p, const float* d_acc, int32_t window_size, double max_norm,
                               const gro_adamw_hparams* hp, int64_t step, float* d_master, float* d_m,
                               float* d_v, uint16_t* d_param_bf16, void* stream) {
   clear_error();
   int rc = check_bound(p);
   if (rc != GRO_OK) return rc;
-  if (hp == nullptr) return set_error(GRO_E_INVALID, "hp is NULL");
-  if (step < 1) return set_error(GRO_E_INVALID, "step must be >= 1");
+  rc = check_step_args(hp, step, max_norm);
+  if (rc != GRO_OK) return rc;
   if (window_size < 1) return set_error(GRO_E_INVALID, "window_size must be >= 1");
-  if (std::isnan(max_norm)) return set_error(GRO_E_INVALID, "max_norm is NaN");
-  if (!(hp->lr >= 0.0) || !std::isfinite(hp->lr) || !(hp->eps >= 0.0) || !std::isfinite(hp->eps) ||
-      !(hp->weight_decay >= 0.0) || !std::isfinite(hp->weight_decay) || !(hp->beta1 >= 0.0) ||
-      !(hp->beta1 < 1.0) || !(hp->beta2 >= 0.0) || !(hp->beta2 < 1.0))
-    return set_error(GRO_E_INVALID, "hyper-parameters out of range (lr, eps, wd >= 0; 0 <= beta < 1)");
-  const bool any = !p->buckets.empty();
-  if (any) {
-    if (d_acc == nullptr || !aligned16(d_acc) || d_master == nullptr || !aligned16(d_master) ||
-        d_m == nullptr || !aligned16(d_m) || d_v == nullptr || !aligned16(d_v) ||
-        (d_param_bf16 != nullptr && !aligned16(d_param_bf16)))
-      return set_error(GRO_E_INVALID, "state pointers must be non-NULL and 16-byte aligned");
-    if (d_acc != p->acc_ptr) return set_error(GRO_E_STATE, "d_acc is not the accumulator of this window");
-  }
-  if (!p->norm_done || p->norm_window != window_size)
-    return set_error(GRO_E_STATE, "gro_reduce_norm of this window (size %d) has not run", window_size);
+  if (!p->buckets.empty() &&
+      (d_acc == nullptr || !aligned16(d_acc) || d_master == nullptr || !aligned16(d_master) || d_m == nullptr ||
+       !aligned16(d_m) || d_v == nullptr || !aligned16(d_v) || (d_param_bf16 != nullptr && !aligned16(d_param_bf16))))
+    return set_error(GRO_E_INVALID, "state pointers must be non-NULL and 16-byte aligned");
+  rc = check_step_state(p, d_acc, window_size);
+  if (rc != GRO_OK) return rc;
 
-  // Per-step scalars in FP64 from the hyper-parameters as given, each rounded
-  // once to FP32.
-  const double bc1 = 1.0 - std::pow(hp->beta1, double(step));
-  const double bc2 = 1.0 - std::pow(hp->beta2, double(step));
+  const AdamWConsts k = adamw_consts(*hp, step, max_norm, window_size);
   AdamWLaunch a;
   std::memset(&a, 0, sizeof(a));
   a.chunks = dev_chunks(p);
@@ -566,20 +606,65 @@ extern "C" int gro_clip_adamw(gro_plan* p, const float* d_acc, int32_t window_si
   a.v = d_v;
   a.p_bf16 = d_param_bf16;
   a.scalars = dev_scalars(p);
-  a.max_norm = max_norm;
-  a.clip_on = (max_norm > 0.0 && !std::isinf(max_norm)) ? 1 : 0;
-  a.window = window_size;
-  a.beta1 = float(hp->beta1);
-  a.beta2 = float(hp->beta2);
-  a.one_minus_beta1 = float(1.0 - hp->beta1);
-  a.one_minus_beta2 = float(1.0 - hp->beta2);
-  a.step_size = float(hp->lr / bc1);
-  a.sqrt_bc2 = float(std::sqrt(bc2));
-  a.eps = float(hp->eps);
-  a.decay = float(1.0 - hp->lr * hp->weight_decay);
+  a.max_norm = k.max_norm;
+  a.clip_on = k.clip_on;
+  a.window = k.window;
+  a.beta1 = k.beta1;
+  a.beta2 = k.beta2;
+  a.one_minus_beta1 = k.one_minus_beta1;
+  a.one_minus_beta2 = k.one_minus_beta2;
+  a.step_size = k.step_size;
+  a.sqrt_bc2 = k.sqrt_bc2;
+  a.eps = k.eps;
+  a.decay = k.decay;
   a.acc_nt = acc_nontemporal(p, GRO_ADAMW_ACC_NT) ? 1 : 0;
   const hipError_t e = launch_adamw(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "clip+AdamW launch");
   reset_window(p);
   return GRO_OK;
+}
+
+extern "C" int gro_clip_adamw_coded(gro_plan* p, const float* d_acc, int32_t window_size, double max_norm,
+                                    const gro_adamw_hparams* hp, int64_t step, float* d_master,
+                                    const gro_coded_moments* moments, uint16_t* d_param_bf16, void* stream) {
+  clear_error();
+  int rc = check_bound(p);
+  if (rc != GRO_OK) return rc;
+  rc = check_step_args(hp, step, max_norm);
+  if (rc != GRO_OK) return rc;
+  if (window_size < 1) return set_error(GRO_E_INVALID, "window_size must be >= 1");
+  if (!p->buckets.empty() && (d_acc == nullptr || !aligned16(d_acc) || d_master == nullptr || !aligned16(d_master) ||
+                              (d_param_bf16 != nullptr && !aligned16(d_param_bf16))))
+    return set_error(GRO_E_INVALID, "state pointers must be non-NULL and 16-byte aligned");
+  rc = check_coded(p, moments, {flat_range(p, d_acc, 4), flat_range(p, d_master, 4), flat_range(p, d_param_bf16, 2)});
+  if (rc != GRO_OK) return rc;
+  rc = check_step_state(p, d_acc, window_size);
+  if (rc != GRO_OK) return rc;
+
+  CodedStepLaunch a;
+  a.chunks = dev_chunks(p);
+  a.buckets = dev_buckets(p);
+  a.n_chunks = int64_t(p->chunks.size());
+  a.acc = d_acc;
+  a.master = d_master;
+  a.moments = *moments;
+  a.p_bf16 = d_param_bf16;
+  a.scalars = dev_scalars(p);
+  a.k = adamw_consts(*hp, step, max_norm, window_size);
+  const hipError_t e = launch_adamw_coded(a, acc_nontemporal(p, GRO_ADAMW_ACC_NT), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "clip+AdamW launch");
+  reset_window(p);
+  return GRO_OK;
+}
+
+extern "C" int gro_moments_encode(gro_plan* p, const float* d_m, const float* d_v, const gro_coded_moments* moments,
+                                  void* stream) {
+  clear_error();
+  return run_moments(p, d_m, d_v, moments, true, stream);
+}
+
+extern "C" int gro_moments_decode(gro_plan* p, const gro_coded_moments* moments, float* d_m, float* d_v,
+                                  void* stream) {
+  clear_error();
+  return run_moments(p, d_m, d_v, moments, false, stream);
 }

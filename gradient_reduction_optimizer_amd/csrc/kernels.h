@@ -83,6 +83,37 @@ struct AdamWLaunch {
   int32_t acc_nt;           // 1: load the accumulator with the non-temporal policy
 };
 
+// One step's scalars, derived once on the host (adamw_consts) and passed to
+// the kernels that hold the moments in codes or take tensors where they lie.
+struct AdamWConsts {
+  double max_norm;
+  int32_t clip_on;
+  int32_t window;
+  float beta1, beta2, one_minus_beta1, one_minus_beta2;
+  float step_size, sqrt_bc2, eps, decay;
+};
+
+struct CodedStepLaunch {
+  const ChunkDev* chunks;
+  const BucketDev* buckets;
+  int64_t n_chunks;
+  const float* acc;
+  float* master;
+  gro_coded_moments moments;
+  uint16_t* p_bf16;         // may be null
+  const double* scalars;
+  AdamWConsts k;
+};
+
+// FP32 moments to codes or back, over a plan's chunks.
+struct MomentsLaunch {
+  const ChunkDev* chunks;
+  int64_t n_chunks;
+  float* m;
+  float* v;
+  gro_coded_moments moments;
+};
+
 struct InitLaunch {
   const ChunkDev* chunks;
   int64_t n_chunks;
@@ -105,5 +136,9 @@ size_t wg_cap_lds_bytes(int32_t cap, int32_t max_lds_per_block);
 hipError_t launch_norm_partials(const NormLaunch& a, hipStream_t s);
 hipError_t launch_norm_final(const NormFinalLaunch& a, hipStream_t s);
 hipError_t launch_adamw(const AdamWLaunch& a, hipStream_t s);
+// acc_nt: load the accumulator with the non-temporal policy.
+hipError_t launch_adamw_coded(const CodedStepLaunch& a, bool acc_nt, hipStream_t s);
+hipError_t launch_moments_encode(const MomentsLaunch& a, hipStream_t s);
+hipError_t launch_moments_decode(const MomentsLaunch& a, hipStream_t s);
 
 }  // namespace gro

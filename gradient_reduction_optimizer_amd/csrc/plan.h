@@ -21,6 +21,11 @@ constexpr int32_t kChunkElems = GRO_CHUNK_ELEMS;
 // (256 B of FP32, 128 B of BF16) so every chunk starts 128-bit aligned.
 constexpr int64_t kAlignElems = 64;
 constexpr int64_t kMaxNumel = int64_t(1) << 46;
+// Elements per scale of 8-bit moments.  A divisor of the alignment, so that no
+// block spans two buckets, and one row of 16 lanes with 4 elements each.
+constexpr int32_t kCodedBlock = GRO_CODED_BLOCK;
+static_assert(kCodedBlock == 64 && kAlignElems % kCodedBlock == 0 && kChunkElems % kCodedBlock == 0,
+              "whole blocks per chunk");
 
 // Device-side tables, uploaded by gro_plan_bind.
 struct ChunkDev {          // 16 B

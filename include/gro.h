@@ -42,14 +42,16 @@
  *    a thread-local message (gro_last_error).  Validation precedes any device
  *    work.  Non-finite data is reported through gro_plan_get_norm's `finite`
  *    flag, not a return code, because device work is asynchronous.
- *  - Only gro_plan_bind, gro_plan_bind_static, gro_init_uniform and
- *    gro_plan_get_norm wait for the device.  The step's calls
- *    (gro_accumulate*, gro_reduce_norm, gro_clip_adamw) only enqueue kernels
+ *  - Only gro_plan_bind, gro_plan_bind_static, gro_init_uniform,
+ *    gro_plan_get_norm, gro_group_bind and gro_group_get_norm wait for the
+ *    device.  The step's calls (gro_accumulate*, gro_reduce_norm,
+ *    gro_clip_adamw, gro_clip_adamw_coded, gro_moments_encode,
+ *    gro_moments_decode, gro_group_norm, gro_group_clip_adamw) only enqueue kernels
  *    -- no allocation, no synchronization, no memory fill -- so a step may be
  *    captured in a HIP graph after binding and replayed; the replay repeats
  *    the captured arguments, the AdamW step count included.
- *  - Not thread-safe per plan; distinct plans may be used from distinct
- *    threads.
+ *  - Not thread-safe per plan or group; distinct ones may be used from
+ *    distinct threads.
  */
 #ifndef GRO_H
 #define GRO_H
@@ -79,6 +81,7 @@ extern "C" {
 #define GRO_NO_DECAY  1u  /* no weight decay for this tensor */
 #define GRO_FROZEN    2u  /* no gradient, not in the norm, not updated */
 #define GRO_FP32_GRAD 4u  /* gradient contributions arrive in FP32 instead of BF16 */
+#define GRO_CODED_MOMENTS 8u  /* groups only: this tensor's moments are held in 8 bits */
 
 /* ---- gradient element types (gro_tensor_layout / gro_bucket_info) ---- */
 #define GRO_GRAD_BF16 0
@@ -334,6 +337,134 @@ int gro_clip_adamw(gro_plan* plan, const float* d_acc, int32_t window_size, doub
  * Waits for its own upload before returning. */
 int gro_init_uniform(gro_plan* plan, uint64_t seed, const double* bounds, const double* offsets,
                      float* d_master, uint16_t* d_param_bf16, void* stream);
+
+/* ---- moments in 8 bits ----
+ * Adam's moments as one code byte per element, with one FP32 scale per moment
+ * and block of GRO_CODED_BLOCK consecutive elements: 2.125 bytes per element
+ * instead of 8.
+ *   m: scale s = max |m| over the block; code = the FP8 e4m3 value (no
+ *      infinities, bias 7) nearest 256 * m / s.  Value: code * (s / 256).  A
+ *      block whose s is below 2^-100 is held as zeros with scale 0.
+ *   v: r = sqrt(v), scale s = max r; code = the unsigned 8-bit float of 4
+ *      exponent bits (bias 15) and 4 mantissa bits, gradual underflow, nearest
+ *      r / s -- the bits 6 to 13 of the FP16 of the same value; 240 is 1.0 and
+ *      nothing above it occurs.  Value: (code * s)^2.  A v > 0 never gets the
+ *      code 0.
+ * Nearest means ties to even; the quotients are FP32, so a value within 2^-22
+ * of the border between two codes may get either.  A block's largest element is held exactly, and
+ * encoding what was decoded gives the same codes and scales (unless a value
+ * leaves FP32's normal range on the way).  m comes back within 2^-4 of itself
+ * or 2^-18 of its block's largest; sqrt(v) within 2^-5 of itself or 2^-18 of
+ * its block's largest.  An infinite v is held as the largest finite one; a
+ * NaN or negative v, or a NaN or infinite m, makes that moment NaN in its
+ * whole block.
+ * In a plan a block is [64 k, 64 k + 64) of the flat arrays -- bucket bases
+ * are multiples of 64, so no block spans two buckets; the part of a block past
+ * the end of its bucket does not enter the scale and its bytes stay as they
+ * are.  In a group's tensor blocks count from the tensor's first element. */
+#define GRO_CODED_BLOCK 64
+
+/* Device pointers of a plan's 8-bit moments: n_flat code bytes each and
+ * n_flat / GRO_CODED_BLOCK scales each (all zeros = moments of zero).  16-byte
+ * aligned; the four arrays, the other arrays of a call and the BF16 copy must
+ * not overlap. */
+typedef struct gro_coded_moments {
+  uint8_t* m;
+  uint8_t* v;
+  float* m_scale;
+  float* v_scale;
+} gro_coded_moments;
+
+/* gro_clip_adamw with the moments in 8 bits: decode, the same update in FP32,
+ * encode, in one pass.  The parameter is updated with the new moments before
+ * they are rounded to codes.  Arguments, order of calls, clipping, the skipped
+ * step of a non-finite norm (codes and scales stay bit-unchanged too) and
+ * errors as gro_clip_adamw; overlapping arrays are GRO_E_INVALID. */
+int gro_clip_adamw_coded(gro_plan* plan, const float* d_acc, int32_t window_size, double max_norm,
+                         const gro_adamw_hparams* hp, int64_t step, float* d_master,
+                         const gro_coded_moments* moments, uint16_t* d_param_bf16, void* stream);
+
+/* FP32 moments of the plan's updated elements to 8 bits and back, for
+ * example around a checkpoint or to change a running job over.  Elements
+ * between buckets are neither read nor written.  No part of a window: may be
+ * called at any time on a bound plan. */
+int gro_moments_encode(gro_plan* plan, const float* d_m, const float* d_v, const gro_coded_moments* moments,
+                       void* stream);
+int gro_moments_decode(gro_plan* plan, const gro_coded_moments* moments, float* d_m, float* d_v, void* stream);
+
+/* ---- groups: tensors that stay where they lie ----
+ * A group steps many tensors at once whose gradients are complete (window
+ * accumulation and reduction done elsewhere, for example by autograd and an
+ * earlier owner) and which are not laid out by a plan: every master, moment,
+ * BF16 copy and gradient is an allocation of its own or a contiguous view at
+ * any element offset. */
+typedef struct gro_group gro_group;
+
+/* One tensor of a group: GRO_NO_DECAY, GRO_FP32_GRAD and GRO_CODED_MOMENTS
+ * may be set. */
+typedef struct gro_group_desc {
+  int64_t numel;
+  uint32_t flags;
+  uint32_t reserved;        /* 0 */
+} gro_group_desc;
+
+/* Device pointers of one tensor, given when the group is bound.  m and v:
+ * FP32, or with GRO_CODED_MOMENTS one code byte per element, and then
+ * m_scale and v_scale hold ceil(numel / GRO_CODED_BLOCK) FP32 scales each
+ * (else unused).  Each array aligned to its own element; a tensor is accessed
+ * four elements at a time when its FP32 arrays are 16-byte, its BF16 ones
+ * 8-byte and its codes 4-byte aligned, and one at a time otherwise. */
+typedef struct gro_group_tensor {
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  uint16_t* param_bf16;     /* may be NULL */
+} gro_group_tensor;
+
+typedef struct gro_group_info {
+  int32_t n_tensors;
+  int32_t chunk_elems;
+  int64_t n_chunks;
+  int64_t n_elems;
+  uint64_t workspace_bytes; /* device workspace gro_group_bind needs */
+} gro_group_info;
+
+/* Host tables for n_tensors tensors (0 elements are allowed and do nothing).
+ * GRO_E_INVALID for negative or too large sizes, GRO_E_PLACEMENT for unknown
+ * flags or a nonzero reserved field. */
+int gro_group_create(const gro_group_desc* tensors, int32_t n_tensors, gro_group** out);
+void gro_group_destroy(gro_group* group);
+int gro_group_get_info(const gro_group* group, gro_group_info* info);
+
+/* Upload the tables into the caller's workspace (>= workspace_bytes, 256-byte
+ * aligned) on `stream` and wait.  tensors: host array of n_tensors entries, read
+ * only during the call.  An array that would be written twice -- a tensor given
+ * twice, or overlapping views -- is GRO_E_DUPLICATE.  May be repeated, for
+ * example when a state has moved. */
+int gro_group_bind(gro_group* group, const gro_group_tensor* tensors, void* d_workspace, uint64_t bytes,
+                   void* stream);
+
+/* Global L2 norm of g = gradient / window_size over the group's tensors, FP64,
+ * no atomics, bit-reproducible, as gro_reduce_norm.  d_grads: host array of
+ * n_tensors device pointers, BF16 or (GRO_FP32_GRAD) FP32, aligned to their
+ * element; NULL leaves that tensor out of this step: not in the norm, not
+ * decayed, not updated.  The gradients have to stay in place until
+ * gro_group_clip_adamw, which reads the same ones; they must not overlap the
+ * arrays the group writes. */
+int gro_group_norm(gro_group* group, const void* const* d_grads, int32_t window_size, void* stream);
+
+/* Clip + AdamW of the gradients given to the last gro_group_norm, per element
+ * as gro_clip_adamw; a non-finite norm leaves everything bit-unchanged.  Needs a
+ * gro_group_norm since the last call (else GRO_E_STATE), on the same stream or
+ * ordered before this one. */
+int gro_group_clip_adamw(gro_group* group, double max_norm, const gro_adamw_hparams* hp, int64_t step,
+                         void* stream);
+
+/* Wait for the stream of the last gro_group_norm and read its norm, as
+ * gro_plan_get_norm. */
+int gro_group_get_norm(gro_group* group, double* norm, double* norm_sq, int32_t* finite);
 
 /* Thread-local text of the last error ("" if none). */
 const char* gro_last_error(void);

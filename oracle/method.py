@@ -269,6 +269,109 @@ def adamw_update(g: np.ndarray, coef, p: np.ndarray, m: np.ndarray, v: np.ndarra
     return p, m, v, f32_to_bf16(p)
 
 
+# ------------------------------------------------------- 8-bit moments
+# Moments in blocks of CODED_BLOCK consecutive elements, one scale each.  Each
+# format is stated as the table of its codes' values; rounding to a code is a
+# search of that table.
+CODED_BLOCK = 64
+SCALE_FLOOR = F32(2.0 ** -100)
+ROOT_MAX = F32(2.0 ** 64 - 2.0 ** 40)   # the largest FP32 whose square is finite
+
+
+def e4m3_values() -> np.ndarray:
+    """Values of the non-negative FP8 e4m3 codes 0..126 (4 exponent bits of
+    bias 7, 3 mantissa bits, gradual underflow); code 127 is NaN."""
+    c = np.arange(127)
+    e, f = c >> 3, (c & 7) / 8.0
+    return np.where(e == 0, f * 2.0 ** -6, (1.0 + f) * 2.0 ** (e - 7.0))
+
+
+def root_values() -> np.ndarray:
+    """Values of the second moments' codes 0..255 (unsigned, 4 exponent bits
+    of bias 15, 4 mantissa bits, gradual underflow); 240 is 1.0."""
+    c = np.arange(256)
+    e, f = c >> 4, (c & 15) / 16.0
+    return np.where(e == 0, f * 2.0 ** -14, (1.0 + f) * 2.0 ** (e - 15.0))
+
+
+def nearest_code(y: np.ndarray, values: np.ndarray) -> np.ndarray:
+    """Index of the value nearest each y >= 0 (ascending `values`), a tie going
+    to the even index.  FP64, in which FP32 inputs and all midpoints are exact."""
+    y = np.asarray(y, dtype=np.float64)
+    lo = np.clip(np.searchsorted(values, y, side="right") - 1, 0, len(values) - 2)
+    below, above = y - values[lo], values[lo + 1] - y
+    return np.where((above < below) | ((above == below) & (lo % 2 == 1)), lo + 1, lo)
+
+
+def _blocks(x: np.ndarray) -> np.ndarray:
+    """Whole blocks [nb, CODED_BLOCK] of a tensor, zeros past its end."""
+    x = np.asarray(x, dtype=F32).ravel()
+    nb = -(-x.size // CODED_BLOCK)
+    out = np.zeros(nb * CODED_BLOCK, dtype=F32)
+    out[:x.size] = x
+    return out.reshape(nb, CODED_BLOCK)
+
+
+def encode_m(m: np.ndarray):
+    """First moments to (codes uint8, scales FP32): s the block's largest |m|,
+    0 when that is below 2^-100; code = e4m3 nearest m * (256 / s)."""
+    m = np.asarray(m, dtype=F32).ravel()
+    b = _blocks(m)
+    with np.errstate(all="ignore"):
+        s = np.max(np.abs(b), axis=1, initial=F32(0))     # NaN if any is NaN
+        s = np.where(s < SCALE_FLOOR, F32(0), s)
+        inv = np.where(s == 0, F32(0), F32(256) / s)
+        y = b * inv[:, None]
+    codes = nearest_code(np.where(np.isnan(y), 0, np.abs(y)), e4m3_values()).astype(np.uint8)
+    codes = np.where(np.isnan(y), 127, codes) | (np.signbit(y).astype(np.uint8) << 7)
+    return codes.astype(np.uint8).reshape(-1)[:m.size], s.astype(F32)
+
+
+def decode_m(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    codes = np.asarray(codes, dtype=np.uint8)
+    v = np.append(e4m3_values(), np.nan)[codes & 127].astype(F32)
+    v = np.where(codes >= 128, -v, v)
+    k = np.asarray(scales, dtype=F32) * F32(1 / 256)
+    return v * np.repeat(k, CODED_BLOCK)[:codes.size]
+
+
+def encode_v(v: np.ndarray):
+    """Second moments to (codes uint8, scales FP32): r = sqrt(v), s the block's
+    largest r (the largest root FP32 can square when it is infinite); code
+    nearest r * (1 / s), at least 1 where r > 0, at most 240."""
+    v = np.asarray(v, dtype=F32).ravel()
+    with np.errstate(all="ignore"):
+        r = np.sqrt(_blocks(v) + F32(0))
+        s = np.max(r, axis=1, initial=F32(0))
+        s = np.where(np.isinf(s), ROOT_MAX, s)
+        inv = np.where(s == 0, F32(0), F32(1) / s)
+        # scaled into FP32's subnormals, where the code's last bit is 2^-130
+        z = (r * inv[:, None]) * F32(2.0 ** -112)
+    # a block with a NaN scale holds NaN whatever its codes are
+    y = np.where(np.isnan(z), 0, np.minimum(np.abs(z).astype(np.float64) * 2.0 ** 112, 1.0))
+    codes = nearest_code(y, root_values())
+    codes = np.where(r > 0, np.maximum(codes, 1), codes)
+    return codes.astype(np.uint8).reshape(-1)[:v.size], s.astype(F32)
+
+
+def decode_v(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    codes = np.asarray(codes, dtype=np.uint8)
+    r = root_values()[codes].astype(F32) * np.repeat(np.asarray(scales, dtype=F32), CODED_BLOCK)[:codes.size]
+    return r * r
+
+
+def adamw_update_coded(g, coef, p, coded, sc: AdamWScalars, decayed: bool):
+    """adamw_update with the moments held in 8 bits, coded = (m codes, v codes,
+    m scales, v scales): decode, the same update, encode.  The parameter uses
+    the moments before they are rounded to codes.
+    Returns (p, coded, p_bf16_bits)."""
+    mc, vc, ms, vs = coded
+    p, m, v, bits = adamw_update(g, coef, p, decode_m(mc, ms), decode_v(vc, vs), sc, decayed)
+    mc, ms = encode_m(m)
+    vc, vs = encode_v(v)
+    return p, (mc, vc, ms, vs), bits
+
+
 # ------------------------------------------------------------- N3 init
 _MASK64 = (1 << 64) - 1
 _PHILOX_M = (0xD2E7470EE14C6C93, 0xCA5A826395121157)
