@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kBlock) void k_group_adamw(const GroupStepLaunch P)
                        CODED ? t.v_scale + b : nullptr,
                        t.pb ? t.pb + ch.begin : nullptr, ch.len};
   const bool wide = t.wide != 0 && (reinterpret_cast<uintptr_t>(g) & (sizeof(typename In::raw_t) - 1)) == 0;
-  step_any<In, CODED>(c, k, wide);
+  step_chunk<In, CODED>(c, k, wide);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@ __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P)
   const StepChunk c = {P.acc + ch.begin, P.master + ch.begin, P.moments.m + ch.begin, P.moments.v + ch.begin,
                        P.moments.m_scale + b, P.moments.v_scale + b,
                        P.p_bf16 ? P.p_bf16 + ch.begin : nullptr, ch.len};
-  step_any<AccIn<NT>, true>(c, k, true);
+  step_chunk<AccIn<NT>, true>(c, k, true);
 }
 
 __global__ __launch_bounds__(kBlock) void k_moments_encode(const MomentsLaunch P) {

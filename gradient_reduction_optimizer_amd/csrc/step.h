@@ -157,5 +157,78 @@ __device__ void step_any(const StepChunk& c, const AdamScalars& k, bool wide) {
   }
 }
 
+// A full chunk of arrays that take four-element accesses, the window division
+// (WM) and the BF16 copy fixed at compile time: kStepUnroll vectors of every
+// array are loaded before any is used, no bounds checks.  Same operations as
+// step_any.
+#ifndef GRO_STEP_UNROLL
+#define GRO_STEP_UNROLL 4
+#endif
+constexpr int kStepUnroll = GRO_STEP_UNROLL;
+static_assert((kChunkElems / 4) % (kStepUnroll * kBlock) == 0, "whole sweeps per chunk");
+
+template <typename In, bool CODED, int WM, bool COPY>
+__device__ __forceinline__ void step_full(const StepChunk& c, const AdamScalars& k) {
+#pragma unroll 1
+  for (int v0 = threadIdx.x; v0 < kChunkElems / 4; v0 += kStepUnroll * kBlock) {
+    typename In::raw_t g[kStepUnroll];
+    f32x4 p[kStepUnroll], m[kStepUnroll], v[kStepUnroll];
+    uint32_t mc[kStepUnroll], vc[kStepUnroll];
+    float ms[kStepUnroll], vs[kStepUnroll];
+#pragma unroll
+    for (int u = 0; u < kStepUnroll; ++u) {
+      const int e = 4 * (v0 + u * kBlock);
+      g[u] = In::load(c.g, e);
+      p[u] = ld4f_nt(c.p + e);
+      if (CODED) {
+        mc[u] = ld1u_nt(c.m, e);
+        vc[u] = ld1u_nt(c.v, e);
+        ms[u] = c.m_scale[e / kCodedBlock];
+        vs[u] = c.v_scale[e / kCodedBlock];
+      } else {
+        m[u] = ld4f_nt(static_cast<const float*>(c.m) + e);
+        v[u] = ld4f_nt(static_cast<const float*>(c.v) + e);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kStepUnroll; ++u) {
+      const int e = 4 * (v0 + u * kBlock);
+      if (CODED) {
+        m[u] = decode_m4(mc[u], ms[u]);
+        v[u] = decode_v4(vc[u], vs[u]);
+      }
+      adamw4<WM>(In::widen(g[u]), p[u], m[u], v[u], k);
+      st4f_nt(c.p + e, p[u]);
+      if (COPY) store_bf16x4(c.pb + e, p[u]);
+      if (CODED) {
+        const Coded4 cm = encode_m4(m[u]);
+        const Coded4 cv = encode_root4(sqrt4(v[u]));
+        st1u_nt(c.m, e, cm.codes);
+        st1u_nt(c.v, e, cv.codes);
+        if ((threadIdx.x & 15) == 0) {
+          c.m_scale[e / kCodedBlock] = cm.scale;
+          c.v_scale[e / kCodedBlock] = cv.scale;
+        }
+      } else {
+        st4f_nt(static_cast<float*>(c.m) + e, m[u]);
+        st4f_nt(static_cast<float*>(c.v) + e, v[u]);
+      }
+    }
+  }
+}
+
+template <typename In, bool CODED>
+__device__ __forceinline__ void step_chunk(const StepChunk& c, const AdamScalars& k, bool wide) {
+  if (!wide || c.len != kChunkElems) {
+    step_any<In, CODED>(c, k, wide);
+  } else if (div_mode(k.wdiv) == kMulInv) {
+    if (c.pb) step_full<In, CODED, kMulInv, true>(c, k);
+    else step_full<In, CODED, kMulInv, false>(c, k);
+  } else {
+    if (c.pb) step_full<In, CODED, kIeeeDiv, true>(c, k);
+    else step_full<In, CODED, kIeeeDiv, false>(c, k);
+  }
+}
+
 }  // namespace
 }  // namespace gro
