@@ -12,43 +12,63 @@
 
 namespace gro {
 
-// Gradient pointers that travel in one norm launch's kernel arguments.
+// Gradient pointers that travel in one launch's kernel arguments (under 4 KB).
 constexpr int kGroupPointers = 448;
 
-struct GroupTensorDev {    // 64 B
+// A chunk of one tensor with everything a kernel needs of it, so that one load
+// leads to the arrays.  Pointers are those of the chunk's first element.
+struct GroupChunkDev {     // 64 B
   float* p;
   void* m;
   void* v;
-  float* m_scale;
+  float* m_scale;          // null for FP32 moments
   float* v_scale;
-  uint16_t* pb;
-  int64_t decayed;
-  int64_t wide;            // every array above takes four-element accesses
+  uint16_t* pb;            // may be null
+  int64_t begin;           // first element within the tensor
+  int32_t tensor;
+  uint16_t len;            // 1..kChunkElems
+  uint16_t flags;
 };
-static_assert(sizeof(GroupTensorDev) == 64, "group tensor entry is 64 bytes");
+static_assert(sizeof(GroupChunkDev) == 64 && kChunkElems <= 65535, "group chunk entry is 64 bytes");
+enum GroupChunkFlag : uint16_t {
+  kChunkDecayed = 1,
+  kChunkFp32 = 2,          // FP32 gradient
+  kChunkWide = 4,          // the arrays above take four-element accesses
+};
 
-struct GroupNormLaunch {
-  const ChunkDev* chunks;  // begin: first element within the tensor; bucket: the tensor
-  int64_t q_begin, q_end;
-  const void** table;      // gradient pointer of every tensor, left for the step
+// Writes n tensors' gradient pointers into the table, from tensor t_first on.
+struct GroupTableLaunch {
+  const void** table;
+  int32_t t_first;
+  int32_t n;
+  const void* grads[kGroupPointers];
+};
+
+struct GroupNormArgs {
+  const GroupChunkDev* chunks;
+  int64_t n_chunks;
+  const void* const* table;   // every tensor's gradient, when not in `grads`
+  const void** chunk_grads;   // out: every chunk's gradient, for the step
   double* partials;
-  int32_t t_first;         // tensor of grads[0]
-  int32_t fp32;            // gradients of the range are FP32
   int32_t window;
-  int32_t reserved;
+};
+struct GroupNormLaunch {
+  GroupNormArgs a;
   const void* grads[kGroupPointers];
 };
 
 struct GroupStepLaunch {
-  const ChunkDev* chunks;
+  const GroupChunkDev* chunks;
   int64_t q_begin, q_end;
-  const GroupTensorDev* tensors;
-  const void* const* table;
+  const void* const* chunk_grads;
   const double* scalars;
   AdamWConsts k;
 };
 
+hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s);
+// With the gradients of all tensors in the arguments, or in the table.
 hipError_t launch_group_norm(const GroupNormLaunch& a, hipStream_t s);
+hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s);
 // The chunks of [q_begin, q_end) all have gradients of one type and moments
 // of one kind.
 hipError_t launch_group_step(const GroupStepLaunch& a, bool fp32, bool coded, hipStream_t s);
@@ -64,13 +84,11 @@ struct gro_group {
     int32_t given;         // index as given
     uint32_t flags;
     int64_t numel;
-    int64_t first_chunk;
   };
   std::vector<Entry> entries;
+  int64_t n_chunks = 0;
   int64_t kind_chunk[5] = {0, 0, 0, 0, 0};  // first chunk of each kind, and the end
-  int32_t kind_entry[5] = {0, 0, 0, 0, 0};
-  std::vector<gro::ChunkDev> chunks;
-  uint64_t scalar_off = 0, tensor_off = 0, table_off = 0, chunk_off = 0, partial_off = 0, group_off = 0,
+  uint64_t scalar_off = 0, table_off = 0, chunk_off = 0, grad_off = 0, partial_off = 0, group_off = 0,
            counter_off = 0, counter_bytes = 0, total = 0;
 
   char* d_ws = nullptr;

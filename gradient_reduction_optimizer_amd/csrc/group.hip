@@ -1,69 +1,149 @@
 // gfx950 kernels of groups: the gradients' norm and clip + AdamW over tensors
-// that stay where they lie.  One workgroup per chunk of up to kChunkElems
-// elements of one tensor, as in a plan; the second stage of the norm is the
-// plan's (launch_norm_final).
+// that stay where they lie.
+//
+// The step takes one workgroup per chunk of up to kChunkElems elements of one
+// tensor, as in a plan.  The norm's first stage takes one wave per chunk: a
+// BF16 chunk is only 8 KB, eight 16-byte loads of each lane, all issued before
+// one is used, and its sum needs no barrier; with one workgroup per chunk and
+// a block sum, launching workgroups and waiting on them took most of the time
+// (37 us for the draft set's 134 MB).  The second stage is the plan's
+// (launch_norm_final).
 #include "group.h"
 #include "step.h"
 
 namespace gro {
 namespace {
 
-// Sum of (g / window)^2 over a chunk, FP64, in a fixed order: a lane's vectors
-// ascending, each vector's elements in order, then the workgroup sum.  A
-// tensor's first chunk also leaves its gradient pointer for the step.
-template <typename In>
-__device__ double group_sumsq(const void* g, int64_t begin, int len, const Divisor& wdiv) {
-  const bool wide = (reinterpret_cast<uintptr_t>(g) & (sizeof(typename In::raw_t) - 1)) == 0;
-  double ss = 0.0;
-  for (int e = 4 * int(threadIdx.x); e < len; e += 4 * kBlock) {
-    const f32x4 x = load_part<In>(g, begin + e, min(len - e, 4), wide);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ss += sq(divide(x[i], wdiv));
+// Gradients of one type, 16 bytes of them at a time.
+struct Bf16Vec {
+  static constexpr int kElems = 8;
+  typedef uint32_t raw_t __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ float get(const raw_t r, int i) {
+    return __uint_as_float((i & 1) ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
   }
+  static __device__ __forceinline__ float load1(const void* g, int e) { return Bf16In::load1(g, e); }
+};
+struct F32Vec {
+  static constexpr int kElems = 4;
+  typedef f32x4 raw_t;
+  static __device__ __forceinline__ float get(const raw_t r, int i) { return r[i]; }
+  static __device__ __forceinline__ float load1(const void* g, int e) { return F32In::load1(g, e); }
+};
+
+// (x / window)^2 added in FP64.  The square of an FP32 value is exact there,
+// so the fused form rounds once, as a product and a sum would.
+__device__ __forceinline__ double add_sq(double ss, float x) { return __builtin_fma(double(x), double(x), ss); }
+
+// This lane's sum over a chunk: vectors lane, lane + 64, ... in order, each
+// vector's elements in order, whichever way they are loaded; a vector that is
+// not there adds zeros.  All loads are issued before one is used.  They keep
+// the default cache policy: the step reads the same gradients next.
+template <typename Vec, int WM>
+__device__ double wave_sumsq(const void* g, int len, bool wide, const Divisor& wdiv) {
+  constexpr int kVecs = kChunkElems / 64 / Vec::kElems;
+  const int lane = int(threadIdx.x) & 63;
+  double ss = 0.0;
+  if (wide) {
+    const int whole = len / Vec::kElems;
+    typename Vec::raw_t x[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      x[j] = typename Vec::raw_t{};
+      if (lane + 64 * j < whole) x[j] = static_cast<const typename Vec::raw_t*>(g)[lane + 64 * j];
+    }
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < Vec::kElems; ++i) ss = add_sq(ss, divide_m<WM>(Vec::get(x[j], i), wdiv));
+    if (lane == whole % 64)  // the lane whose next vector is cut off
+      for (int e = whole * Vec::kElems; e < len; ++e) ss = add_sq(ss, divide_m<WM>(Vec::load1(g, e), wdiv));
+    return ss;
+  }
+  for (int v = lane; v * Vec::kElems < len; v += 64)
+    for (int e = v * Vec::kElems; e < min(len, (v + 1) * Vec::kElems); ++e)
+      ss = add_sq(ss, divide_m<WM>(Vec::load1(g, e), wdiv));
   return ss;
 }
 
-__global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch P) {
-  const int64_t q = P.q_begin + int64_t(blockIdx.x);
-  const ChunkDev ch = P.chunks[q];
-  const void* g = P.grads[ch.bucket - P.t_first];
-  if (ch.begin == 0 && threadIdx.x == 0) P.table[ch.bucket] = g;
+template <typename Vec>
+__device__ double wave_sumsq_window(const void* g, int len, const Divisor& wdiv) {
+  const bool wide = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
+  return wdiv.pow2 ? wave_sumsq<Vec, kMulInv>(g, len, wide, wdiv) : wave_sumsq<Vec, kIeeeDiv>(g, len, wide, wdiv);
+}
+
+// One wave: the partial of chunk q, and its gradient pointer for the step.
+__device__ void norm_chunk(const GroupNormArgs& P, int64_t q, const GroupChunkDev& ch, const void* tensor_grad) {
+  const bool fp32 = (ch.flags & kChunkFp32) != 0;
+  const char* g = static_cast<const char*>(tensor_grad);
   double ss = 0.0;
   if (g != nullptr) {
+    g += ch.begin * (fp32 ? 4 : 2);
     const Divisor wdiv = make_divisor(P.window);
-    ss = P.fp32 ? group_sumsq<F32In>(g, ch.begin, ch.len, wdiv) : group_sumsq<Bf16In>(g, ch.begin, ch.len, wdiv);
+    ss = fp32 ? wave_sumsq_window<F32Vec>(g, ch.len, wdiv) : wave_sumsq_window<Bf16Vec>(g, ch.len, wdiv);
   }
-  const double t = block_sum(ss);
-  if (threadIdx.x == 0) P.partials[q] = t;
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) ss += __shfl_xor(ss, m, 64);
+  if ((threadIdx.x & 63) == 0) {
+    P.partials[q] = ss;
+    P.chunk_grads[q] = g;
+  }
+}
+
+// Chunk of this wave; the wave's number is the same in all of its lanes.
+__device__ __forceinline__ int64_t chunk_of_wave() {
+  return int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+}
+
+__global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch P) {
+  const int64_t q = chunk_of_wave();
+  if (q >= P.a.n_chunks) return;
+  const GroupChunkDev ch = P.a.chunks[q];
+  norm_chunk(P.a, q, ch, P.grads[ch.tensor]);
+}
+
+__global__ __launch_bounds__(kBlock) void k_group_norm_table(const GroupNormArgs P) {
+  const int64_t q = chunk_of_wave();
+  if (q >= P.n_chunks) return;
+  const GroupChunkDev ch = P.chunks[q];
+  norm_chunk(P, q, ch, P.table[ch.tensor]);
+}
+
+__global__ __launch_bounds__(kBlock) void k_group_table(const GroupTableLaunch P) {
+  const int i = int(blockIdx.x) * kBlock + int(threadIdx.x);
+  if (i < P.n) P.table[P.t_first + i] = P.grads[i];
 }
 
 template <typename In, bool CODED>
 __global__ __launch_bounds__(kBlock) void k_group_adamw(const GroupStepLaunch P) {
   const int64_t q = P.q_end - 1 - int64_t(blockIdx.x);  // last to first: the norm has just read the last gradients
+  const GroupChunkDev ch = P.chunks[q];
+  const void* g = P.chunk_grads[q];
   if (P.scalars[kFinite] == 0.0) return;                // non-finite norm: skip the step
-  const ChunkDev ch = P.chunks[q];
-  const void* g = P.table[ch.bucket];
   if (g == nullptr) return;                             // left out of this step
-  const GroupTensorDev t = P.tensors[ch.bucket];
-  const AdamScalars k = step_scalars(P.k, P.scalars, t.decayed != 0);
-  constexpr int64_t moment = CODED ? 1 : sizeof(float);
-  const int64_t b = ch.begin / kCodedBlock;
-  const StepChunk c = {static_cast<const char*>(g) + ch.begin * int64_t(sizeof(typename In::raw_t) / 4),
-                       t.p + ch.begin,
-                       static_cast<char*>(t.m) + ch.begin * moment,
-                       static_cast<char*>(t.v) + ch.begin * moment,
-                       CODED ? t.m_scale + b : nullptr,
-                       CODED ? t.v_scale + b : nullptr,
-                       t.pb ? t.pb + ch.begin : nullptr, ch.len};
-  const bool wide = t.wide != 0 && (reinterpret_cast<uintptr_t>(g) & (sizeof(typename In::raw_t) - 1)) == 0;
+  const AdamScalars k = step_scalars(P.k, P.scalars, (ch.flags & kChunkDecayed) != 0);
+  const StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
+  const bool wide =
+      (ch.flags & kChunkWide) != 0 && (reinterpret_cast<uintptr_t>(g) & (sizeof(typename In::raw_t) - 1)) == 0;
   step_chunk<In, CODED>(c, k, wide);
 }
 
 }  // namespace
 
+hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s) {
+  if (a.n <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_group_table, dim3(unsigned((a.n + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_group_norm(const GroupNormLaunch& a, hipStream_t s) {
-  if (a.q_end <= a.q_begin) return hipSuccess;
-  hipLaunchKernelGGL(k_group_norm, dim3(unsigned(a.q_end - a.q_begin)), dim3(kBlock), 0, s, a);
+  if (a.a.n_chunks <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_group_norm, dim3(unsigned((a.a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s) {
+  if (a.n_chunks <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_group_norm_table, dim3(unsigned((a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
 

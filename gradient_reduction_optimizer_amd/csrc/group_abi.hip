@@ -29,64 +29,65 @@ int check_group(const gro_group* g) {
 }
 
 double* dev_scalars(const gro_group* g) { return reinterpret_cast<double*>(g->d_ws + g->scalar_off); }
-const ChunkDev* dev_chunks(const gro_group* g) { return reinterpret_cast<const ChunkDev*>(g->d_ws + g->chunk_off); }
+const GroupChunkDev* dev_chunks(const gro_group* g) {
+  return reinterpret_cast<const GroupChunkDev*>(g->d_ws + g->chunk_off);
+}
 const void** dev_table(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->table_off); }
+const void** dev_grads(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->grad_off); }
 double* dev_partials(const gro_group* g) { return reinterpret_cast<double*>(g->d_ws + g->partial_off); }
+
+int64_t chunks_of(int64_t numel) { return (numel + kChunkElems - 1) / kChunkElems; }
 
 int fill_group(gro_group* g, const gro_group_desc* tensors, int32_t n) {
   g->n_tensors = n;
-  int64_t n_chunks = 0;
   for (int32_t i = 0; i < n; ++i) {
     const gro_group_desc& d = tensors[i];
     if (d.numel < 0 || d.numel > kMaxNumel)
       return set_error(GRO_E_INVALID, "tensor %d: %lld elements", i, (long long)d.numel);
     if ((d.flags & ~(GRO_NO_DECAY | GRO_FP32_GRAD | GRO_CODED_MOMENTS)) || d.reserved != 0)
       return set_error(GRO_E_PLACEMENT, "tensor %d: unknown flags 0x%x or nonzero reserved field", i, d.flags);
-    n_chunks += (d.numel + kChunkElems - 1) / kChunkElems;
+    g->n_chunks += chunks_of(d.numel);
     // one workgroup of kBlock lanes per chunk, fewer than 2^32 lanes a launch
-    if (n_chunks >= (int64_t(1) << 24) - 1)
+    if (g->n_chunks >= (int64_t(1) << 24) - 1)
       return set_error(GRO_E_INVALID, "group too large: more chunks than one launch grid addresses");
     g->n_elems += d.numel;
   }
-  g->chunks.reserve(size_t(n_chunks));
+  int64_t q = 0;
   for (int kind = 0; kind < 4; ++kind) {
-    g->kind_chunk[kind] = int64_t(g->chunks.size());
-    g->kind_entry[kind] = int32_t(g->entries.size());
+    g->kind_chunk[kind] = q;
     for (int32_t i = 0; i < n; ++i) {
       const gro_group_desc& d = tensors[i];
       if (d.numel == 0 || kind_of(d.flags) != kind) continue;
-      const int32_t t = int32_t(g->entries.size());
-      g->entries.push_back(gro_group::Entry{i, d.flags, d.numel, int64_t(g->chunks.size())});
-      for (int64_t off = 0; off < d.numel; off += kChunkElems)
-        g->chunks.push_back(ChunkDev{off, int32_t(std::min<int64_t>(d.numel - off, kChunkElems)), t});
+      g->entries.push_back(gro_group::Entry{i, d.flags, d.numel});
+      q += chunks_of(d.numel);
     }
   }
-  g->kind_chunk[4] = int64_t(g->chunks.size());
-  g->kind_entry[4] = int32_t(g->entries.size());
+  g->kind_chunk[4] = q;
 
-  const int64_t groups = norm_groups(int64_t(g->chunks.size()));
   uint64_t off = 0;
   const auto place = [&off](uint64_t bytes) {
     const uint64_t at = off;
     off = uint64_t(align_up(int64_t(off + bytes), 256));
     return at;
   };
+  const uint64_t chunks = uint64_t(g->n_chunks);
   g->scalar_off = place(256);
-  g->tensor_off = place(g->entries.size() * sizeof(GroupTensorDev));
   g->table_off = place(g->entries.size() * sizeof(void*));
-  g->chunk_off = place(g->chunks.size() * sizeof(ChunkDev));
-  g->partial_off = place(g->chunks.size() * sizeof(double));
-  g->group_off = place(uint64_t(groups) * sizeof(double));
+  g->chunk_off = place(chunks * sizeof(GroupChunkDev));
+  g->grad_off = place(chunks * sizeof(void*));
+  g->partial_off = place(chunks * sizeof(double));
+  g->group_off = place(uint64_t(norm_groups(g->n_chunks)) * sizeof(double));
   g->counter_bytes = 256;
   g->counter_off = place(g->counter_bytes);
   g->total = off;
   return GRO_OK;
 }
 
-// Device table entries of the live tensors from the caller's pointers.
-int fill_tensors(const gro_group* g, const gro_group_tensor* tensors, std::vector<GroupTensorDev>& out) {
+// The device chunk table from the caller's pointers.
+int fill_chunks(const gro_group* g, const gro_group_tensor* tensors, std::vector<GroupChunkDev>& out) {
   std::vector<Range> written;
   written.reserve(g->entries.size() * 6);
+  int32_t index = 0;
   for (const gro_group::Entry& e : g->entries) {
     const gro_group_tensor& t = tensors[e.given];
     const bool coded = (e.flags & GRO_CODED_MOMENTS) != 0;
@@ -98,6 +99,7 @@ int fill_tensors(const gro_group* g, const gro_group_tensor* tensors, std::vecto
     if (coded && (t.m_scale == nullptr || t.v_scale == nullptr || !aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4)))
       return set_error(GRO_E_INVALID, "tensor %d: scales of 8-bit moments are NULL or not 4-byte aligned", e.given);
     const uint64_t n = uint64_t(e.numel);
+    const uint64_t scales = coded ? (n + kCodedBlock - 1) / kCodedBlock * sizeof(float) : 0;
     const auto add = [&written](const void* a, uint64_t bytes) {
       if (a != nullptr) written.push_back(Range{reinterpret_cast<uintptr_t>(a), bytes});
     };
@@ -105,22 +107,26 @@ int fill_tensors(const gro_group* g, const gro_group_tensor* tensors, std::vecto
     add(t.m, n * moment);
     add(t.v, n * moment);
     add(t.param_bf16, n * 2);
-    if (coded) {
-      const uint64_t scales = (n + kCodedBlock - 1) / kCodedBlock * sizeof(float);
-      add(t.m_scale, scales);
-      add(t.v_scale, scales);
+    add(t.m_scale, scales);
+    add(t.v_scale, scales);
+    const bool wide = aligned_to(t.master, 16) && aligned_to(t.m, 4 * moment) && aligned_to(t.v, 4 * moment) &&
+                      aligned_to(t.param_bf16, 8);
+    for (int64_t begin = 0; begin < e.numel; begin += kChunkElems) {
+      GroupChunkDev c;
+      c.p = t.master + begin;
+      c.m = static_cast<char*>(t.m) + begin * int64_t(moment);
+      c.v = static_cast<char*>(t.v) + begin * int64_t(moment);
+      c.m_scale = coded ? t.m_scale + begin / kCodedBlock : nullptr;
+      c.v_scale = coded ? t.v_scale + begin / kCodedBlock : nullptr;
+      c.pb = t.param_bf16 ? t.param_bf16 + begin : nullptr;
+      c.begin = begin;
+      c.tensor = index;
+      c.len = uint16_t(std::min<int64_t>(e.numel - begin, kChunkElems));
+      c.flags = uint16_t(((e.flags & GRO_NO_DECAY) ? 0 : kChunkDecayed) |
+                         ((e.flags & GRO_FP32_GRAD) ? kChunkFp32 : 0) | (wide ? kChunkWide : 0));
+      out.push_back(c);
     }
-    GroupTensorDev d;
-    d.p = t.master;
-    d.m = t.m;
-    d.v = t.v;
-    d.m_scale = coded ? t.m_scale : nullptr;
-    d.v_scale = coded ? t.v_scale : nullptr;
-    d.pb = t.param_bf16;
-    d.decayed = (e.flags & GRO_NO_DECAY) ? 0 : 1;
-    d.wide = aligned_to(t.master, 16) && aligned_to(t.m, 4 * moment) && aligned_to(t.v, 4 * moment) &&
-             aligned_to(t.param_bf16, 8);
-    out.push_back(d);
+    ++index;
   }
   if (first_overlap(written.data(), written.size()) >= 0)
     return set_error(GRO_E_DUPLICATE, "two of the group's arrays overlap: an element would be updated twice");
@@ -128,9 +134,9 @@ int fill_tensors(const gro_group* g, const gro_group_tensor* tensors, std::vecto
 }
 
 int bind_group(gro_group* g, const gro_group_tensor* tensors, char* ws, hipStream_t s) {
-  std::vector<GroupTensorDev> table;
-  table.reserve(g->entries.size());
-  const int rc = fill_tensors(g, tensors, table);
+  std::vector<GroupChunkDev> chunks;
+  chunks.reserve(size_t(g->n_chunks));
+  const int rc = fill_chunks(g, tensors, chunks);
   if (rc != GRO_OK) return rc;
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
@@ -139,10 +145,8 @@ int bind_group(gro_group* g, const gro_group_tensor* tensors, char* ws, hipStrea
   // counts returns it there.
   g->bound = false;
   e = hipMemsetAsync(ws + g->counter_off, 0, g->counter_bytes, s);
-  if (e == hipSuccess && !table.empty())
-    e = hipMemcpyAsync(ws + g->tensor_off, table.data(), table.size() * sizeof(GroupTensorDev), hipMemcpyHostToDevice, s);
-  if (e == hipSuccess && !g->chunks.empty())
-    e = hipMemcpyAsync(ws + g->chunk_off, g->chunks.data(), g->chunks.size() * sizeof(ChunkDev), hipMemcpyHostToDevice, s);
+  if (e == hipSuccess && !chunks.empty())
+    e = hipMemcpyAsync(ws + g->chunk_off, chunks.data(), chunks.size() * sizeof(GroupChunkDev), hipMemcpyHostToDevice, s);
   const hipError_t done = hipStreamSynchronize(s);
   if (e == hipSuccess) e = done;
   if (e != hipSuccess) return hip_fail(e, "gro_group_bind upload");
@@ -183,7 +187,7 @@ extern "C" int gro_group_get_info(const gro_group* g, gro_group_info* info) {
   std::memset(info, 0, sizeof(*info));
   info->n_tensors = g->n_tensors;
   info->chunk_elems = kChunkElems;
-  info->n_chunks = int64_t(g->chunks.size());
+  info->n_chunks = g->n_chunks;
   info->n_elems = g->n_elems;
   info->workspace_bytes = g->total;
   return GRO_OK;
@@ -217,35 +221,43 @@ extern "C" int gro_group_norm(gro_group* g, const void* const* d_grads, int32_t 
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   g->norm_done = false;  // from here on the pointers of an earlier call are being replaced
-  const auto first_chunk = [g](int32_t t) {
-    return t < int32_t(g->entries.size()) ? g->entries[size_t(t)].first_chunk : int64_t(g->chunks.size());
+  GroupNormArgs a;
+  a.chunks = dev_chunks(g);
+  a.n_chunks = g->n_chunks;
+  a.table = dev_table(g);
+  a.chunk_grads = dev_grads(g);
+  a.partials = dev_partials(g);
+  a.window = window_size;
+  const int32_t n = int32_t(g->entries.size());
+  const auto copy = [&](const void** to, int32_t first, int32_t count) {
+    for (int32_t i = 0; i < count; ++i) to[i] = d_grads[g->entries[size_t(first + i)].given];
   };
-  for (int half = 0; half < 2; ++half) {  // BF16 gradients, then FP32 ones
-    const int32_t end = g->kind_entry[2 * half + 2];
-    for (int32_t t = g->kind_entry[2 * half]; t < end; t += kGroupPointers) {
-      const int32_t te = std::min(end, t + kGroupPointers);
-      GroupNormLaunch a;
-      std::memset(&a, 0, sizeof(a));
-      a.chunks = dev_chunks(g);
-      a.q_begin = first_chunk(t);
-      a.q_end = first_chunk(te);
-      a.table = dev_table(g);
-      a.partials = dev_partials(g);
-      a.t_first = t;
-      a.fp32 = half;
-      a.window = window_size;
-      for (int32_t i = t; i < te; ++i) a.grads[i - t] = d_grads[g->entries[size_t(i)].given];
-      const hipError_t e = launch_group_norm(a, s);
-      if (e != hipSuccess) return hip_fail(e, "group norm launch");
+  hipError_t e = hipSuccess;
+  if (n <= kGroupPointers) {
+    GroupNormLaunch l;
+    std::memset(&l, 0, sizeof(l));
+    l.a = a;
+    copy(l.grads, 0, n);
+    e = launch_group_norm(l, s);
+  } else {
+    GroupTableLaunch l;
+    l.table = dev_table(g);
+    for (int32_t t = 0; t < n && e == hipSuccess; t += kGroupPointers) {
+      l.t_first = t;
+      l.n = std::min(n - t, int32_t(kGroupPointers));
+      copy(l.grads, t, l.n);
+      e = launch_group_table(l, s);
     }
+    if (e == hipSuccess) e = launch_group_norm_table(a, s);
   }
+  if (e != hipSuccess) return hip_fail(e, "group norm launch");
   NormFinalLaunch f;
   f.partials = dev_partials(g);
-  f.n_chunks = int64_t(g->chunks.size());
+  f.n_chunks = g->n_chunks;
   f.group_sums = reinterpret_cast<double*>(g->d_ws + g->group_off);
   f.counter = reinterpret_cast<uint32_t*>(g->d_ws + g->counter_off);
   f.scalars = dev_scalars(g);
-  const hipError_t e = launch_norm_final(f, s);
+  e = launch_norm_final(f, s);
   if (e != hipSuccess) return hip_fail(e, "group norm stage-2 launch");
   g->norm_done = true;
   g->norm_valid = true;
@@ -264,8 +276,7 @@ extern "C" int gro_group_clip_adamw(gro_group* g, double max_norm, const gro_ada
   if (!g->norm_done) return set_error(GRO_E_STATE, "gro_group_norm of this step has not run");
   GroupStepLaunch a;
   a.chunks = dev_chunks(g);
-  a.tensors = reinterpret_cast<const GroupTensorDev*>(g->d_ws + g->tensor_off);
-  a.table = dev_table(g);
+  a.chunk_grads = dev_grads(g);
   a.scalars = dev_scalars(g);
   a.k = adamw_consts(*hp, step, max_norm, g->window);
   for (int kind = 0; kind < 4; ++kind) {
