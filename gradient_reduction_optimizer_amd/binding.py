@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Iterable, List, Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -404,7 +405,10 @@ def gro_group_norm(group: int, d_grads: Sequence[int], window_size: int = 1, str
     """d_grads: one pointer per tensor, 0 for a tensor that has no gradient in
     this step."""
     n = gro_group_get_info(group)["n_tensors"]
-    ptrs = _pointer_array(d_grads, n, "gro_group_norm")
+    if len(d_grads) != n:
+        raise ValueError(f"gro_group_norm: {len(d_grads)} pointers given, the call reads {n}")
+    flat = array("Q", d_grads)  # a group has thousands of tensors: one conversion of the whole list
+    ptrs = (ctypes.c_void_p * n).from_buffer(flat) if n else None
     _check(load().gro_group_norm(ctypes.c_void_p(group), ptrs, int(window_size), ctypes.c_void_p(stream)))
 
 

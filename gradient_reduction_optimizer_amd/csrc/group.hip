@@ -113,18 +113,34 @@ __global__ __launch_bounds__(kBlock) void k_group_table(const GroupTableLaunch P
   if (i < P.n) P.table[P.t_first + i] = P.grads[i];
 }
 
-template <typename In, bool CODED>
-__global__ __launch_bounds__(kBlock) void k_group_adamw(const GroupStepLaunch P) {
-  const int64_t q = P.q_end - 1 - int64_t(blockIdx.x);  // last to first: the norm has just read the last gradients
+// At least 4 waves per SIMD (at most 128 registers): the path of cut-off chunks
+// would take a few more than that and cost every chunk a wave.
+template <typename In, bool CODED, bool SPLIT>
+__global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch P) {
+  // last to first: the norm has just read the last gradients
+  const int64_t q = P.q_end - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
   const GroupChunkDev ch = P.chunks[q];
   const void* g = P.chunk_grads[q];
-  if (P.scalars[kFinite] == 0.0) return;                // non-finite norm: skip the step
-  if (g == nullptr) return;                             // left out of this step
+  if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
+  if (g == nullptr) return;               // left out of this step
   const AdamScalars k = step_scalars(P.k, P.scalars, (ch.flags & kChunkDecayed) != 0);
-  const StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
+  StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
+  if (SPLIT) {
+    take_part<In, CODED>(c, int(blockIdx.x & 3));
+    if (c.len == 0) return;
+  }
   const bool wide =
       (ch.flags & kChunkWide) != 0 && (reinterpret_cast<uintptr_t>(g) & (sizeof(typename In::raw_t) - 1)) == 0;
-  step_chunk<In, CODED>(c, k, wide);
+  step_chunk<In, CODED, SPLIT>(c, k, wide);
+}
+
+template <typename In, bool CODED>
+void group_step(const GroupStepLaunch& a, hipStream_t s) {
+  const int64_t n = a.q_end - a.q_begin;
+  if (n <= kSplitChunks)
+    hipLaunchKernelGGL((k_group_adamw<In, CODED, true>), dim3(unsigned(4 * n)), dim3(kBlock), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_group_adamw<In, CODED, false>), dim3(unsigned(n)), dim3(kBlock), 0, s, a);
 }
 
 }  // namespace
@@ -149,11 +165,10 @@ hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s) {
 
 hipError_t launch_group_step(const GroupStepLaunch& a, bool fp32, bool coded, hipStream_t s) {
   if (a.q_end <= a.q_begin) return hipSuccess;
-  const dim3 grid(unsigned(a.q_end - a.q_begin)), block(kBlock);
-  if (fp32 && coded) hipLaunchKernelGGL((k_group_adamw<F32In, true>), grid, block, 0, s, a);
-  else if (fp32) hipLaunchKernelGGL((k_group_adamw<F32In, false>), grid, block, 0, s, a);
-  else if (coded) hipLaunchKernelGGL((k_group_adamw<Bf16In, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_group_adamw<Bf16In, false>), grid, block, 0, s, a);
+  if (fp32 && coded) group_step<F32In, true>(a, s);
+  else if (fp32) group_step<F32In, false>(a, s);
+  else if (coded) group_step<Bf16In, true>(a, s);
+  else group_step<Bf16In, false>(a, s);
   return hipGetLastError();
 }
 

@@ -6,70 +6,133 @@
 namespace gro {
 namespace {
 
-template <bool NT>
+template <bool NT, bool SPLIT>
 __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P) {
-  const int64_t q = P.n_chunks - 1 - int64_t(blockIdx.x);  // last to first, as k_adamw
-  if (P.scalars[kFinite] == 0.0) return;                   // non-finite norm: skip the step
+  // last to first, as k_adamw
+  const int64_t q = P.n_chunks - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
   const ChunkDev ch = P.chunks[q];
+  if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
   const AdamScalars k = step_scalars(P.k, P.scalars, P.buckets[ch.bucket].decayed != 0);
   const int64_t b = ch.begin / kCodedBlock;
-  const StepChunk c = {P.acc + ch.begin, P.master + ch.begin, P.moments.m + ch.begin, P.moments.v + ch.begin,
-                       P.moments.m_scale + b, P.moments.v_scale + b,
-                       P.p_bf16 ? P.p_bf16 + ch.begin : nullptr, ch.len};
-  step_chunk<AccIn<NT>, true>(c, k, true);
+  StepChunk c = {P.acc + ch.begin, P.master + ch.begin, P.moments.m + ch.begin, P.moments.v + ch.begin,
+                 P.moments.m_scale + b, P.moments.v_scale + b,
+                 P.p_bf16 ? P.p_bf16 + ch.begin : nullptr, ch.len};
+  if (SPLIT) {
+    take_part<AccIn<NT>, true>(c, int(blockIdx.x & 3));
+    if (c.len == 0) return;
+  }
+  step_chunk<AccIn<NT>, true, SPLIT>(c, k, true);
 }
 
+// Conversions: U vectors per lane, kChunkElems / (U * kPartElems) workgroups
+// per chunk.  Decoding takes 1 (97k elements 2.4 us against 2.9 with 2 and 3.5
+// with 4; 67M elements 114 us, 123, 113), encoding, which waits for its block's
+// maximum, 2 (97k 3.5 us against 2.9 with 1 and 4.5 with 4; 167M elements 277
+// us, 289, 283).
+#ifndef GRO_ENCODE_VECS
+#define GRO_ENCODE_VECS 2
+#endif
+#ifndef GRO_DECODE_VECS
+#define GRO_DECODE_VECS 1
+#endif
+constexpr int kEncodeVecs = GRO_ENCODE_VECS;
+constexpr int kDecodeVecs = GRO_DECODE_VECS;
+static_assert(kVecsPerLane % kEncodeVecs == 0 && kVecsPerLane % kDecodeVecs == 0, "whole workgroups per chunk");
+
+// This workgroup's stretch of a chunk: flat index of its first element, and
+// how many elements it has (may be none).
+template <int U>
+__device__ __forceinline__ int moments_part(const MomentsLaunch& P, int64_t& begin) {
+  constexpr int parts = kVecsPerLane / U;
+  const ChunkDev ch = P.chunks[blockIdx.x / parts];
+  const int off = int(blockIdx.x % parts) * (U * kPartElems);
+  begin = ch.begin + off;
+  return min(ch.len - off, U * kPartElems);
+}
+
+template <int U>
 __global__ __launch_bounds__(kBlock) void k_moments_encode(const MomentsLaunch P) {
-  const ChunkDev ch = P.chunks[blockIdx.x];
-  const int trips = (ch.len + 4 * kBlock - 1) / (4 * kBlock);
-  for (int t = 0; t < trips; ++t) {
-    const int e = 4 * (t * kBlock + int(threadIdx.x));
-    const int n = min(max(ch.len - e, 0), 4);
-    const f32x4 m = load_part<F32In>(P.m + ch.begin, e, n, true);
-    // + 0: a root of -0 would have the largest bits of all
-    const f32x4 v = load_part<F32In>(P.v + ch.begin, e, n, true) + f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const Coded4 cm = encode_m4(m);
-    const Coded4 cv = encode_root4(sqrt4(v));
-    store_codes(P.moments.m + ch.begin, e, n, true, cm.codes);
-    store_codes(P.moments.v + ch.begin, e, n, true, cv.codes);
+  int64_t begin;
+  const int len = moments_part<U>(P, begin);
+  if (len <= 0) return;
+  f32x4 m[U], v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = min(max(len - e, 0), 4);
+    m[u] = load_part<F32In>(P.m + begin, e, n, true);
+    v[u] = load_part<F32In>(P.v + begin, e, n, true);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = min(max(len - e, 0), 4);
+    const Coded4 cm = encode_m4(m[u]);
+    // + 0: the root of -0 would have the largest bits of all
+    const Coded4 cv = encode_root4(sqrt4(v[u] + f32x4{0.0f, 0.0f, 0.0f, 0.0f}));
+    store_codes(P.moments.m + begin, e, n, true, cm.codes);
+    store_codes(P.moments.v + begin, e, n, true, cv.codes);
     if ((threadIdx.x & 15) == 0 && n > 0) {
-      const int64_t b = (ch.begin + e) / kCodedBlock;
+      const int64_t b = (begin + e) / kCodedBlock;
       P.moments.m_scale[b] = cm.scale;
       P.moments.v_scale[b] = cv.scale;
     }
   }
 }
 
+template <int U>
 __global__ __launch_bounds__(kBlock) void k_moments_decode(const MomentsLaunch P) {
-  const ChunkDev ch = P.chunks[blockIdx.x];
-  for (int e = 4 * int(threadIdx.x); e < ch.len; e += 4 * kBlock) {
-    const int n = min(ch.len - e, 4);
-    const int64_t b = (ch.begin + e) / kCodedBlock;
-    const uint32_t cm = load_codes(P.moments.m + ch.begin, e, n, true);
-    const uint32_t cv = load_codes(P.moments.v + ch.begin, e, n, true);
-    store_part(P.m + ch.begin, e, n, true, decode_m4(cm, P.moments.m_scale[b]));
-    store_part(P.v + ch.begin, e, n, true, decode_v4(cv, P.moments.v_scale[b]));
+  int64_t begin;
+  const int len = moments_part<U>(P, begin);
+  uint32_t mc[U], vc[U];
+  float ms[U], vs[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = min(max(len - e, 0), 4);
+    const int64_t b = (begin + e) / kCodedBlock;
+    mc[u] = load_codes(P.moments.m + begin, e, n, true);
+    vc[u] = load_codes(P.moments.v + begin, e, n, true);
+    ms[u] = n > 0 ? P.moments.m_scale[b] : 0.0f;
+    vs[u] = n > 0 ? P.moments.v_scale[b] : 0.0f;
   }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = min(max(len - e, 0), 4);
+    store_part(P.m + begin, e, n, true, decode_m4(mc[u], ms[u]));
+    store_part(P.v + begin, e, n, true, decode_v4(vc[u], vs[u]));
+  }
+}
+
+template <bool NT>
+void adamw_coded(const CodedStepLaunch& a, hipStream_t s) {
+  if (a.n_chunks <= kSplitChunks)
+    hipLaunchKernelGGL((k_adamw_coded<NT, true>), dim3(unsigned(4 * a.n_chunks)), dim3(kBlock), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_adamw_coded<NT, false>), dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_adamw_coded(const CodedStepLaunch& a, bool acc_nt, hipStream_t s) {
   if (a.n_chunks <= 0) return hipSuccess;
-  if (acc_nt) hipLaunchKernelGGL(k_adamw_coded<true>, dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
-  else hipLaunchKernelGGL(k_adamw_coded<false>, dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
+  if (acc_nt) adamw_coded<true>(a, s);
+  else adamw_coded<false>(a, s);
   return hipGetLastError();
 }
 
 hipError_t launch_moments_encode(const MomentsLaunch& a, hipStream_t s) {
   if (a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_moments_encode, dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL(k_moments_encode<kEncodeVecs>, dim3(unsigned(a.n_chunks * (kVecsPerLane / kEncodeVecs))), dim3(kBlock), 0, s,
+                     a);
   return hipGetLastError();
 }
 
 hipError_t launch_moments_decode(const MomentsLaunch& a, hipStream_t s) {
   if (a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_moments_decode, dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL(k_moments_decode<kDecodeVecs>, dim3(unsigned(a.n_chunks * (kVecsPerLane / kDecodeVecs))), dim3(kBlock), 0, s,
+                     a);
   return hipGetLastError();
 }
 

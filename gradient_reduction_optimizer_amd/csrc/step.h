@@ -113,121 +113,170 @@ __device__ __forceinline__ f32x4 sqrt4(const f32x4 v) {
   return f32x4{sqrtf(v.x), sqrtf(v.y), sqrtf(v.z), sqrtf(v.w)};
 }
 
-// Any chunk: any length, any element-aligned arrays (`wide`: all of them may
-// be accessed four elements at a time).  Every lane makes every trip, because
-// a block's maximum needs its whole row of lanes; elements past the end enter
-// as zeros and are not stored.
+// A chunk of any length whose arrays are only element-aligned, one element at a
+// time.  Every lane makes every trip, because a block's maximum needs its
+// whole row of lanes; elements past the end enter as zeros and are not stored.
 template <typename In, bool CODED>
-__device__ void step_any(const StepChunk& c, const AdamScalars& k, bool wide) {
+__device__ void step_any(const StepChunk& c, const AdamScalars& k) {
   const int trips = (c.len + 4 * kBlock - 1) / (4 * kBlock);
   for (int t = 0; t < trips; ++t) {
     const int e = 4 * (t * kBlock + int(threadIdx.x));
     const int n = min(max(c.len - e, 0), 4);
     const int b = e / kCodedBlock;
-    f32x4 g = load_part<In>(c.g, e, n, wide);
-    f32x4 p = load_part<F32In>(c.p, e, n, wide);
+    f32x4 g = load_part<In>(c.g, e, n, false);
+    f32x4 p = load_part<F32In>(c.p, e, n, false);
     f32x4 m, v;
     if (CODED) {
-      m = decode_m4(load_codes(c.m, e, n, wide), n > 0 ? c.m_scale[b] : 0.0f);
-      v = decode_v4(load_codes(c.v, e, n, wide), n > 0 ? c.v_scale[b] : 0.0f);
+      m = decode_m4(load_codes(c.m, e, n, false), n > 0 ? c.m_scale[b] : 0.0f);
+      v = decode_v4(load_codes(c.v, e, n, false), n > 0 ? c.v_scale[b] : 0.0f);
     } else {
-      m = load_part<F32In>(c.m, e, n, wide);
-      v = load_part<F32In>(c.v, e, n, wide);
+      m = load_part<F32In>(c.m, e, n, false);
+      v = load_part<F32In>(c.v, e, n, false);
     }
     adamw4<kNoDiv>(g, p, m, v, k);
-    store_part(c.p, e, n, wide, p);
-    if (c.pb) store_copy(c.pb, e, n, wide, p);
+    store_part(c.p, e, n, false, p);
+    if (c.pb) store_copy(c.pb, e, n, false, p);
     if (CODED) {
-      const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i >= n) m[i] = v[i] = none[i];
+        if (i >= n) m[i] = v[i] = 0.0f;
       const Coded4 cm = encode_m4(m);
       const Coded4 cv = encode_root4(sqrt4(v));
-      store_codes(c.m, e, n, wide, cm.codes);
-      store_codes(c.v, e, n, wide, cv.codes);
+      store_codes(c.m, e, n, false, cm.codes);
+      store_codes(c.v, e, n, false, cv.codes);
       if ((threadIdx.x & 15) == 0 && n > 0) {
         c.m_scale[b] = cm.scale;
         c.v_scale[b] = cv.scale;
       }
     } else {
-      store_part(static_cast<float*>(c.m), e, n, wide, m);
-      store_part(static_cast<float*>(c.v), e, n, wide, v);
+      store_part(static_cast<float*>(c.m), e, n, false, m);
+      store_part(static_cast<float*>(c.v), e, n, false, v);
     }
   }
 }
 
-// A full chunk of arrays that take four-element accesses, the window division
-// (WM) and the BF16 copy fixed at compile time: kStepUnroll vectors of every
-// array are loaded before any is used, no bounds checks.  Same operations as
+// U vectors per lane of arrays that take four-element accesses: a stretch of
+// U * kPartElems elements, of which `len` are there.  FULL: all of them, and the
+// window division (WM) and the BF16 copy (COPY) are fixed at compile time: no
+// bounds checks.  Every load is issued before one is used.  Same operations as
 // step_any.
-#ifndef GRO_STEP_UNROLL
-#define GRO_STEP_UNROLL 4
-#endif
-constexpr int kStepUnroll = GRO_STEP_UNROLL;
-static_assert((kChunkElems / 4) % (kStepUnroll * kBlock) == 0, "whole sweeps per chunk");
+constexpr int kPartElems = 4 * kBlock;  // one vector per lane
+constexpr int kVecsPerLane = kChunkElems / kPartElems;
+static_assert(kVecsPerLane == 4 && kChunkElems == 4 * kPartElems, "a chunk is four vectors per lane");
+static_assert(kPartElems % kCodedBlock == 0, "whole blocks per quarter chunk");
+enum CopyMode { kNoCopy = 0, kCopy = 1, kMaybeCopy = 2 };
 
-template <typename In, bool CODED, int WM, bool COPY>
-__device__ __forceinline__ void step_full(const StepChunk& c, const AdamScalars& k) {
-#pragma unroll 1
-  for (int v0 = threadIdx.x; v0 < kChunkElems / 4; v0 += kStepUnroll * kBlock) {
-    typename In::raw_t g[kStepUnroll];
-    f32x4 p[kStepUnroll], m[kStepUnroll], v[kStepUnroll];
-    uint32_t mc[kStepUnroll], vc[kStepUnroll];
-    float ms[kStepUnroll], vs[kStepUnroll];
+template <typename In, bool CODED, int U, bool FULL, int WM, int COPY>
+__device__ __forceinline__ void step_wide(const StepChunk& c, const AdamScalars& k) {
+  f32x4 g[U], p[U], m[U], v[U];
+  typename In::raw_t raw[U];
+  uint32_t mc[U], vc[U];
+  float ms[U], vs[U];
 #pragma unroll
-    for (int u = 0; u < kStepUnroll; ++u) {
-      const int e = 4 * (v0 + u * kBlock);
-      g[u] = In::load(c.g, e);
+  for (int u = 0; u < U; ++u) {
+    if (!FULL && u > 0 && u * kPartElems >= c.len) break;
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = FULL ? 4 : min(max(c.len - e, 0), 4);
+    if (FULL) {
+      raw[u] = In::load(c.g, e);
       p[u] = ld4f_nt(c.p + e);
-      if (CODED) {
-        mc[u] = ld1u_nt(c.m, e);
-        vc[u] = ld1u_nt(c.v, e);
-        ms[u] = c.m_scale[e / kCodedBlock];
-        vs[u] = c.v_scale[e / kCodedBlock];
-      } else {
-        m[u] = ld4f_nt(static_cast<const float*>(c.m) + e);
-        v[u] = ld4f_nt(static_cast<const float*>(c.v) + e);
-      }
+    } else {
+      g[u] = load_part<In>(c.g, e, n, true);
+      p[u] = load_part<F32In>(c.p, e, n, true);
     }
+    if (CODED) {
+      mc[u] = FULL ? ld1u_nt(c.m, e) : load_codes(c.m, e, n, true);
+      vc[u] = FULL ? ld1u_nt(c.v, e) : load_codes(c.v, e, n, true);
+      ms[u] = n > 0 ? c.m_scale[e / kCodedBlock] : 0.0f;
+      vs[u] = n > 0 ? c.v_scale[e / kCodedBlock] : 0.0f;
+    } else if (FULL) {
+      m[u] = ld4f_nt(static_cast<const float*>(c.m) + e);
+      v[u] = ld4f_nt(static_cast<const float*>(c.v) + e);
+    } else {
+      m[u] = load_part<F32In>(c.m, e, n, true);
+      v[u] = load_part<F32In>(c.v, e, n, true);
+    }
+  }
 #pragma unroll
-    for (int u = 0; u < kStepUnroll; ++u) {
-      const int e = 4 * (v0 + u * kBlock);
-      if (CODED) {
-        m[u] = decode_m4(mc[u], ms[u]);
-        v[u] = decode_v4(vc[u], vs[u]);
+  for (int u = 0; u < U; ++u) {
+    if (!FULL && u > 0 && u * kPartElems >= c.len) break;
+    const int e = 4 * (int(threadIdx.x) + u * kBlock);
+    const int n = FULL ? 4 : min(max(c.len - e, 0), 4);
+    if (FULL) g[u] = In::widen(raw[u]);
+    if (CODED) {
+      m[u] = decode_m4(mc[u], ms[u]);
+      v[u] = decode_v4(vc[u], vs[u]);
+    }
+    adamw4<WM>(g[u], p[u], m[u], v[u], k);
+    store_part(c.p, e, n, true, p[u]);
+    if (COPY == kCopy || (COPY == kMaybeCopy && c.pb)) store_copy(c.pb, e, n, true, p[u]);
+    if (CODED) {
+      if (!FULL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= n) m[u][i] = v[u][i] = 0.0f;
       }
-      adamw4<WM>(In::widen(g[u]), p[u], m[u], v[u], k);
-      st4f_nt(c.p + e, p[u]);
-      if (COPY) store_bf16x4(c.pb + e, p[u]);
-      if (CODED) {
-        const Coded4 cm = encode_m4(m[u]);
-        const Coded4 cv = encode_root4(sqrt4(v[u]));
-        st1u_nt(c.m, e, cm.codes);
-        st1u_nt(c.v, e, cv.codes);
-        if ((threadIdx.x & 15) == 0) {
-          c.m_scale[e / kCodedBlock] = cm.scale;
-          c.v_scale[e / kCodedBlock] = cv.scale;
-        }
-      } else {
-        st4f_nt(static_cast<float*>(c.m) + e, m[u]);
-        st4f_nt(static_cast<float*>(c.v) + e, v[u]);
+      const Coded4 cm = encode_m4(m[u]);
+      const Coded4 cv = encode_root4(sqrt4(v[u]));
+      store_codes(c.m, e, n, true, cm.codes);
+      store_codes(c.v, e, n, true, cv.codes);
+      if ((threadIdx.x & 15) == 0 && n > 0) {
+        c.m_scale[e / kCodedBlock] = cm.scale;
+        c.v_scale[e / kCodedBlock] = cv.scale;
       }
+    } else {
+      store_part(static_cast<float*>(c.m), e, n, true, m[u]);
+      store_part(static_cast<float*>(c.v), e, n, true, v[u]);
     }
   }
 }
 
-template <typename In, bool CODED>
+// A chunk by one workgroup: all of it in one sweep of four vectors per lane.
+// SPLIT: a quarter of it, for few chunks (see kSplitChunks).
+template <typename In, bool CODED, bool SPLIT>
 __device__ __forceinline__ void step_chunk(const StepChunk& c, const AdamScalars& k, bool wide) {
-  if (!wide || c.len != kChunkElems) {
-    step_any<In, CODED>(c, k, wide);
+  if (!wide) {
+    step_any<In, CODED>(c, k);
+  } else if (SPLIT) {
+    step_wide<In, CODED, 1, false, kNoDiv, kMaybeCopy>(c, k);
+  } else if (c.len != kChunkElems) {
+    step_wide<In, CODED, kVecsPerLane, false, kNoDiv, kMaybeCopy>(c, k);
   } else if (div_mode(k.wdiv) == kMulInv) {
-    if (c.pb) step_full<In, CODED, kMulInv, true>(c, k);
-    else step_full<In, CODED, kMulInv, false>(c, k);
+    if (c.pb) step_wide<In, CODED, kVecsPerLane, true, kMulInv, kCopy>(c, k);
+    else step_wide<In, CODED, kVecsPerLane, true, kMulInv, kNoCopy>(c, k);
   } else {
-    if (c.pb) step_full<In, CODED, kIeeeDiv, true>(c, k);
-    else step_full<In, CODED, kIeeeDiv, false>(c, k);
+    if (c.pb) step_wide<In, CODED, kVecsPerLane, true, kIeeeDiv, kCopy>(c, k);
+    else step_wide<In, CODED, kVecsPerLane, true, kIeeeDiv, kNoCopy>(c, k);
   }
+}
+
+// Up to this many chunks a step takes four workgroups per chunk, one vector
+// per lane each, instead of one with four: few workgroups leave most of the 256
+// CUs idle, and a lane's four vectors are four times the arithmetic in a row.
+// Group steps of n full chunks, split against whole, us: n = 16, 32-bit
+// moments 3.9 / 5.3, 8-bit 5.5 / 6.4; n = 64 5.5 / 5.9 and 5.9 / 6.7; n = 128
+// 6.6 / 6.3 and 6.8 / 7.0; n = 256 8.0 / 7.7 and 8.3 / 7.7; n = 4096 78 / 78 and
+// 70 / 52.
+#ifndef GRO_SPLIT_CHUNKS
+#define GRO_SPLIT_CHUNKS 128
+#endif
+constexpr int64_t kSplitChunks = GRO_SPLIT_CHUNKS;
+
+// The part of a chunk that workgroup `part` of the four takes.
+template <typename In, bool CODED>
+__device__ __forceinline__ void take_part(StepChunk& c, int part) {
+  const int e = part * kPartElems;
+  constexpr int moment = CODED ? 1 : int(sizeof(float));
+  c.g = static_cast<const char*>(c.g) + e * int(sizeof(typename In::raw_t) / 4);
+  c.p += e;
+  c.m = static_cast<char*>(c.m) + e * moment;
+  c.v = static_cast<char*>(c.v) + e * moment;
+  if (CODED) {
+    c.m_scale += e / kCodedBlock;
+    c.v_scale += e / kCodedBlock;
+  }
+  if (c.pb) c.pb += e;
+  c.len = min(max(c.len - e, 0), kPartElems);
 }
 
 }  // namespace
