@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
   const void* g = P.chunk_grads[q];
   if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
   if (g == nullptr) return;               // left out of this step
-  const AdamScalars k = step_scalars(P.k, P.scalars, (ch.flags & kChunkDecayed) != 0);
+  const StepScalars k = step_scalars(P.k, P.scalars, (ch.flags & kChunkDecayed) != 0);
   StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
   if (SPLIT) {
     take_part<In, CODED>(c, int(blockIdx.x & 3));

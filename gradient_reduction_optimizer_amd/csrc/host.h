@@ -47,6 +47,7 @@ inline AdamWConsts adamw_consts(const gro_adamw_hparams& hp, int64_t step, doubl
   k.one_minus_beta2 = float(1.0 - hp.beta2);
   k.step_size = float(hp.lr / bc1);
   k.sqrt_bc2 = float(std::sqrt(bc2));
+  k.inv_sqrt_bc2 = 1.0f / k.sqrt_bc2;
   k.eps = float(hp.eps);
   k.decay = float(1.0 - hp.lr * hp.weight_decay);
   return k;

@@ -90,7 +90,7 @@ struct AdamWConsts {
   int32_t clip_on;
   int32_t window;
   float beta1, beta2, one_minus_beta1, one_minus_beta2;
-  float step_size, sqrt_bc2, eps, decay;
+  float step_size, sqrt_bc2, inv_sqrt_bc2, eps, decay;
 };
 
 struct CodedStepLaunch {

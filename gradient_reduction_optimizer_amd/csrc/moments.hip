@@ -12,7 +12,7 @@ __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P)
   const int64_t q = P.n_chunks - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
   const ChunkDev ch = P.chunks[q];
   if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
-  const AdamScalars k = step_scalars(P.k, P.scalars, P.buckets[ch.bucket].decayed != 0);
+  const StepScalars k = step_scalars(P.k, P.scalars, P.buckets[ch.bucket].decayed != 0);
   const int64_t b = ch.begin / kCodedBlock;
   StepChunk c = {P.acc + ch.begin, P.master + ch.begin, P.moments.m + ch.begin, P.moments.v + ch.begin,
                  P.moments.m_scale + b, P.moments.v_scale + b,
@@ -48,6 +48,10 @@ __device__ __forceinline__ int moments_part(const MomentsLaunch& P, int64_t& beg
   const int off = int(blockIdx.x % parts) * (U * kPartElems);
   begin = ch.begin + off;
   return min(ch.len - off, U * kPartElems);
+}
+
+__device__ __forceinline__ f32x4 sqrt4(const f32x4 v) {
+  return f32x4{sqrtf(v.x), sqrtf(v.y), sqrtf(v.z), sqrtf(v.w)};
 }
 
 template <int U>

@@ -10,9 +10,13 @@
 namespace gro {
 namespace {
 
+struct StepScalars : AdamScalars {
+  float inv_sbc2;      // 1 / sbc2 rounded to nearest
+};
+
 // The step's scalars with the clip coefficient of the norm on the device.
-__device__ __forceinline__ AdamScalars step_scalars(const AdamWConsts& c, const double* scalars, bool decayed) {
-  AdamScalars k;
+__device__ __forceinline__ StepScalars step_scalars(const AdamWConsts& c, const double* scalars, bool decayed) {
+  StepScalars k;
   k.wdiv = make_divisor(c.window);
   k.coef = 1.0f;
   if (c.clip_on) {
@@ -26,8 +30,62 @@ __device__ __forceinline__ AdamScalars step_scalars(const AdamWConsts& c, const 
   k.omb2 = c.one_minus_beta2;
   k.step_size = c.step_size;
   k.sbc2 = c.sqrt_bc2;
+  k.inv_sbc2 = c.inv_sqrt_bc2;
   k.eps = c.eps;
   return k;
+}
+
+// r = sqrt(v) and q = r / sbc2, both rounded to nearest as the IEEE operations
+// round.  For v from 2^-96 to the largest finite value, which is every v of a
+// vector but in odd cases, with fewer issue slots (18 instead of 32):
+//   r: the hardware reciprocal root y, g = v y, r = g + (v - g^2) y/2.  Equal to
+//      the IEEE root for every FP32 in that range (all of them compared on a
+//      gfx950); below, v - g^2 would round.
+//   q: Markstein's division by a number whose reciprocal is rounded to nearest
+//      (IBM J. Res. Dev. 34, 1990): a quotient within one step of the true one,
+//      which the first correction gives, and one more correction round to
+//      nearest.  r lies in [2^-48, 2^64] and sbc2 in [2^-27, 1], so no
+//      remainder leaves the normal range.
+__device__ __forceinline__ void roots4(const f32x4 v, const StepScalars& k, f32x4& r, f32x4& q) {
+  const uint32_t b0 = __float_as_uint(v.x), b1 = __float_as_uint(v.y), b2 = __float_as_uint(v.z),
+                 b3 = __float_as_uint(v.w);
+  constexpr uint32_t kLow = 0x0f800000u, kInf = 0x7f800000u;  // 2^-96, infinity
+  if (min(min(b0, b1), min(b2, b3)) >= kLow && max(max(b0, b1), max(b2, b3)) < kInf) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float y = __builtin_amdgcn_rsqf(v[e]);
+      const float g = v[e] * y;
+      r[e] = __builtin_fmaf(__builtin_fmaf(-g, g, v[e]), 0.5f * y, g);
+      float t = r[e] * k.inv_sbc2;
+      t = __builtin_fmaf(__builtin_fmaf(-t, k.sbc2, r[e]), k.inv_sbc2, t);
+      q[e] = __builtin_fmaf(__builtin_fmaf(-t, k.sbc2, r[e]), k.inv_sbc2, t);
+    }
+  } else {  // zeros, NaN, infinities and roots below 2^-48
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[e] = sqrtf(v[e]);
+      q[e] = r[e] / k.sbc2;
+    }
+  }
+}
+
+// adamw_elem's operations on four elements; r returns sqrt(v) of the new v.
+template <int WM>
+__device__ __forceinline__ void step4(const f32x4 a, f32x4& p, f32x4& m, f32x4& v, f32x4& r, const StepScalars& k) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float g = WM == kNoDiv ? divide(a[e], k.wdiv) : divide_m<WM>(a[e], k.wdiv);
+    const float gh = g * k.coef;
+    m[e] = k.b1 * m[e] + k.omb1 * gh;
+    v[e] = k.b2 * v[e] + k.omb2 * (gh * gh);
+  }
+  f32x4 q;
+  roots4(v, k, r, q);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float d = q[e] + k.eps;
+    p[e] = p[e] * k.decay - k.step_size * (m[e] / d);
+  }
 }
 
 // The gradient as an FP32 accumulator, with the load policy it was stored for.
@@ -109,15 +167,11 @@ __device__ __forceinline__ void store_copy(uint16_t* a, int64_t e, int n, bool w
     if (i < n) a[e + i] = bf16_bits(p[i]);
 }
 
-__device__ __forceinline__ f32x4 sqrt4(const f32x4 v) {
-  return f32x4{sqrtf(v.x), sqrtf(v.y), sqrtf(v.z), sqrtf(v.w)};
-}
-
 // A chunk of any length whose arrays are only element-aligned, one element at a
 // time.  Every lane makes every trip, because a block's maximum needs its
 // whole row of lanes; elements past the end enter as zeros and are not stored.
 template <typename In, bool CODED>
-__device__ void step_any(const StepChunk& c, const AdamScalars& k) {
+__device__ void step_any(const StepChunk& c, const StepScalars& k) {
   const int trips = (c.len + 4 * kBlock - 1) / (4 * kBlock);
   for (int t = 0; t < trips; ++t) {
     const int e = 4 * (t * kBlock + int(threadIdx.x));
@@ -133,15 +187,16 @@ __device__ void step_any(const StepChunk& c, const AdamScalars& k) {
       m = load_part<F32In>(c.m, e, n, false);
       v = load_part<F32In>(c.v, e, n, false);
     }
-    adamw4<kNoDiv>(g, p, m, v, k);
+    f32x4 r;
+    step4<kNoDiv>(g, p, m, v, r, k);
     store_part(c.p, e, n, false, p);
     if (c.pb) store_copy(c.pb, e, n, false, p);
     if (CODED) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i >= n) m[i] = v[i] = 0.0f;
+        if (i >= n) m[i] = r[i] = 0.0f;
       const Coded4 cm = encode_m4(m);
-      const Coded4 cv = encode_root4(sqrt4(v));
+      const Coded4 cv = encode_root4(r);
       store_codes(c.m, e, n, false, cm.codes);
       store_codes(c.v, e, n, false, cv.codes);
       if ((threadIdx.x & 15) == 0 && n > 0) {
@@ -167,7 +222,7 @@ static_assert(kPartElems % kCodedBlock == 0, "whole blocks per quarter chunk");
 enum CopyMode { kNoCopy = 0, kCopy = 1, kMaybeCopy = 2 };
 
 template <typename In, bool CODED, int U, bool FULL, int WM, int COPY>
-__device__ __forceinline__ void step_wide(const StepChunk& c, const AdamScalars& k) {
+__device__ __forceinline__ void step_wide(const StepChunk& c, const StepScalars& k) {
   f32x4 g[U], p[U], m[U], v[U];
   typename In::raw_t raw[U];
   uint32_t mc[U], vc[U];
@@ -207,17 +262,18 @@ __device__ __forceinline__ void step_wide(const StepChunk& c, const AdamScalars&
       m[u] = decode_m4(mc[u], ms[u]);
       v[u] = decode_v4(vc[u], vs[u]);
     }
-    adamw4<WM>(g[u], p[u], m[u], v[u], k);
+    f32x4 r;
+    step4<WM>(g[u], p[u], m[u], v[u], r, k);
     store_part(c.p, e, n, true, p[u]);
     if (COPY == kCopy || (COPY == kMaybeCopy && c.pb)) store_copy(c.pb, e, n, true, p[u]);
     if (CODED) {
       if (!FULL) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (i >= n) m[u][i] = v[u][i] = 0.0f;
+          if (i >= n) m[u][i] = r[i] = 0.0f;
       }
       const Coded4 cm = encode_m4(m[u]);
-      const Coded4 cv = encode_root4(sqrt4(v[u]));
+      const Coded4 cv = encode_root4(r);
       store_codes(c.m, e, n, true, cm.codes);
       store_codes(c.v, e, n, true, cv.codes);
       if ((threadIdx.x & 15) == 0 && n > 0) {
@@ -234,7 +290,7 @@ __device__ __forceinline__ void step_wide(const StepChunk& c, const AdamScalars&
 // A chunk by one workgroup: all of it in one sweep of four vectors per lane.
 // SPLIT: a quarter of it, for few chunks (see kSplitChunks).
 template <typename In, bool CODED, bool SPLIT>
-__device__ __forceinline__ void step_chunk(const StepChunk& c, const AdamScalars& k, bool wide) {
+__device__ __forceinline__ void step_chunk(const StepChunk& c, const StepScalars& k, bool wide) {
   if (!wide) {
     step_any<In, CODED>(c, k);
   } else if (SPLIT) {

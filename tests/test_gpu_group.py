@@ -372,6 +372,34 @@ def test_bound_again_to_moved_states():
             same_bits(host(x), y, "the old place")
 
 
+@pytest.mark.parametrize("step,beta2", [(1, 0.5), (9, 0.5), (3, 0.999), (1, 0.9999999)])
+def test_every_root_of_two_binades(step, beta2):
+    """Root, division by sqrt(bc2) and division of the moments for every FP32
+    mantissa at an even and an odd exponent, and at values outside the range
+    that the short form takes (zeros, subnormals, up to infinity): the same
+    bits as one IEEE operation after the other.  No gradient, no decay, eps 0,
+    p = 0, so that p is -step_size * (m / (sqrt(v) / sqrt(bc2)))."""
+    bits = np.arange(1 << 24, dtype=np.uint32)
+    v = np.concatenate([(bits + np.uint32(0x3f000000)), (bits + np.uint32(0x0f000000)),
+                        np.uint32(0x0f800000) - bits[:5000], bits[:5000], np.uint32(0x7f800000) - bits[:5000],
+                        np.linspace(0, 0x7f800000, 2_000_003).astype(np.uint32)]).view(F32)
+    rng = np.random.default_rng(step)
+    m = rng.uniform(-2, 2, v.size).astype(F32)
+    hp = dict(HP, beta1=0.5, beta2=beta2, eps=0.0, weight_decay=0.0)
+    sc = M.adamw_scalars(*[hp[k] for k in ("lr", "beta1", "beta2", "eps", "weight_decay")], step)
+    with np.errstate(all="ignore"):
+        p, mw, vw, _ = M.adamw_update(np.zeros_like(m), F32(1), np.zeros_like(m), m, v, sc, True)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    pd, state = torch.zeros(v.size, device="cuda"), (dev(m), dev(v))
+    group = TensorGroup([pd], grad_dtype=FP32, states=[state])
+    group.norm([torch.zeros(v.size, device="cuda")])
+    group.clip_adamw(1.0, hp, step)
+    torch.cuda.synchronize()
+    same_bits(host(state[1]), vw, "v")
+    same_bits(host(state[0]), mw, "m")
+    same_bits(host(pd), p, "p")
+
+
 @pytest.mark.parametrize("bits,dtype", [(8, BF16), (32, FP32)])
 def test_offsets_past_32_bits(bits, dtype):
     """A tensor of more than 2^31 elements: both ends against the oracle."""
