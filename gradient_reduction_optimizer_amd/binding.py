@@ -335,30 +335,27 @@ def gro_init_uniform(plan: int, seed: int, bounds: Sequence[float], offsets: Opt
 def _coded(moments: Sequence[int]) -> gro_coded_moments:
     if len(moments) != 4:
         raise ValueError(f"8-bit moments are four pointers (m, v, m_scale, v_scale), got {len(moments)}")
-    return gro_coded_moments(*[int(p) for p in moments])
+    return gro_coded_moments(*moments)
 
 
 def gro_clip_adamw_coded(plan: int, d_acc: int, window_size: int, max_norm: float, hp: dict, step: int,
                          d_master: int, moments: Sequence[int], d_param_bf16: int = 0, stream: int = 0) -> None:
     """moments: the pointers (m, v, m_scale, v_scale) of the 8-bit moments."""
     h, c = _hparams(hp), _coded(moments)
-    _check(load().gro_clip_adamw_coded(ctypes.c_void_p(plan), ctypes.c_void_p(d_acc), int(window_size),
-                                       float(max_norm), ctypes.byref(h), int(step), ctypes.c_void_p(d_master),
-                                       ctypes.byref(c), ctypes.c_void_p(d_param_bf16 or 0), ctypes.c_void_p(stream)))
+    _check(load().gro_clip_adamw_coded(plan, d_acc, int(window_size), float(max_norm), ctypes.byref(h), int(step),
+                                       d_master, ctypes.byref(c), d_param_bf16 or 0, stream))
 
 
 def gro_moments_encode(plan: int, d_m: int, d_v: int, moments: Sequence[int], stream: int = 0) -> None:
     """FP32 moments of a plan to 8-bit ones (pointers m, v, m_scale, v_scale)."""
     c = _coded(moments)
-    _check(load().gro_moments_encode(ctypes.c_void_p(plan), ctypes.c_void_p(d_m), ctypes.c_void_p(d_v),
-                                     ctypes.byref(c), ctypes.c_void_p(stream)))
+    _check(load().gro_moments_encode(plan, d_m, d_v, ctypes.byref(c), stream))
 
 
 def gro_moments_decode(plan: int, moments: Sequence[int], d_m: int, d_v: int, stream: int = 0) -> None:
     """8-bit moments of a plan (pointers m, v, m_scale, v_scale) to FP32 ones."""
     c = _coded(moments)
-    _check(load().gro_moments_decode(ctypes.c_void_p(plan), ctypes.byref(c), ctypes.c_void_p(d_m),
-                                     ctypes.c_void_p(d_v), ctypes.c_void_p(stream)))
+    _check(load().gro_moments_decode(plan, ctypes.byref(c), d_m, d_v, stream))
 
 
 def gro_group_create(tensors: Sequence) -> int:
@@ -378,12 +375,12 @@ def gro_group_create(tensors: Sequence) -> int:
 
 def gro_group_destroy(group: int) -> None:
     if group:
-        load().gro_group_destroy(ctypes.c_void_p(group))
+        load().gro_group_destroy(group)
 
 
 def gro_group_get_info(group: int) -> dict:
     info = gro_group_info()
-    _check(load().gro_group_get_info(ctypes.c_void_p(group), ctypes.byref(info)))
+    _check(load().gro_group_get_info(group, ctypes.byref(info)))
     return _struct_dict(info)
 
 
@@ -397,29 +394,29 @@ def gro_group_bind(group: int, tensors: Sequence[Sequence[int]], d_workspace: in
     rows = (gro_group_tensor * max(n, 1))()
     for i, t in enumerate(tensors):
         rows[i] = gro_group_tensor(*[int(p) for p in t])
-    _check(load().gro_group_bind(ctypes.c_void_p(group), rows, ctypes.c_void_p(d_workspace), int(nbytes),
-                                 ctypes.c_void_p(stream)))
+    _check(load().gro_group_bind(group, rows, d_workspace, int(nbytes), stream))
 
 
 def gro_group_norm(group: int, d_grads: Sequence[int], window_size: int = 1, stream: int = 0) -> None:
     """d_grads: one pointer per tensor, 0 for a tensor that has no gradient in
     this step."""
-    n = gro_group_get_info(group)["n_tensors"]
+    info = gro_group_info()
+    _check(load().gro_group_get_info(group, ctypes.byref(info)))
+    n = info.n_tensors
     if len(d_grads) != n:
         raise ValueError(f"gro_group_norm: {len(d_grads)} pointers given, the call reads {n}")
     flat = array("Q", d_grads)  # a group has thousands of tensors: one conversion of the whole list
     ptrs = (ctypes.c_void_p * n).from_buffer(flat) if n else None
-    _check(load().gro_group_norm(ctypes.c_void_p(group), ptrs, int(window_size), ctypes.c_void_p(stream)))
+    _check(load().gro_group_norm(group, ptrs, int(window_size), stream))
 
 
 def gro_group_clip_adamw(group: int, max_norm: float, hp: dict, step: int, stream: int = 0) -> None:
     h = _hparams(hp)
-    _check(load().gro_group_clip_adamw(ctypes.c_void_p(group), float(max_norm), ctypes.byref(h), int(step),
-                                       ctypes.c_void_p(stream)))
+    _check(load().gro_group_clip_adamw(group, float(max_norm), ctypes.byref(h), int(step), stream))
 
 
 def gro_group_get_norm(group: int):
     """Returns (norm, norm_sq, finite)."""
     n, sq, f = ctypes.c_double(), ctypes.c_double(), ctypes.c_int32()
-    _check(load().gro_group_get_norm(ctypes.c_void_p(group), ctypes.byref(n), ctypes.byref(sq), ctypes.byref(f)))
+    _check(load().gro_group_get_norm(group, ctypes.byref(n), ctypes.byref(sq), ctypes.byref(f)))
     return n.value, sq.value, bool(f.value)

@@ -52,22 +52,35 @@ struct GroupNormArgs {
   double* partials;
   int32_t window;
 };
+template <int N>
 struct GroupNormLaunch {
   GroupNormArgs a;
-  const void* grads[kGroupPointers];
+  const void* grads[N];
 };
+// Most groups' pointers fit the short form, whose launch copies 512 bytes
+// instead of 3.6 KB.
+constexpr int kGroupPointersShort = 64;
 
 struct GroupStepLaunch {
   const GroupChunkDev* chunks;
   int64_t q_begin, q_end;
   const void* const* chunk_grads;
   const double* scalars;
+  const double* partials;  // n_partials > 0: the norm's partials, added up by
+  int32_t n_partials;      // every workgroup itself (see kFoldChunks)
   AdamWConsts k;
 };
 
+// In a group of up to this many chunks the step's workgroups add the norm's
+// partials up themselves, in the order of the second stage (so to the same
+// bits), and no second stage is launched: a launch of 3.7 us that read 128
+// numbers at most.
+constexpr int64_t kFoldChunks = 128;
+
 hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s);
 // With the gradients of all tensors in the arguments, or in the table.
-hipError_t launch_group_norm(const GroupNormLaunch& a, hipStream_t s);
+template <int N>
+hipError_t launch_group_norm(const GroupNormLaunch<N>& a, hipStream_t s);
 hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s);
 // The chunks of [q_begin, q_end) all have gradients of one type and moments
 // of one kind.
@@ -94,7 +107,7 @@ struct gro_group {
   char* d_ws = nullptr;
   bool bound = false;
   int device = -1;
-  bool norm_done = false;   // gradients and norm of a step are on the device
+  bool norm_done = false;   // gradients and norm (or its partials) of a step are on the device
   bool norm_valid = false;  // some norm has been computed since binding
   int32_t window = 0;
   void* norm_stream = nullptr;

@@ -94,7 +94,8 @@ __device__ __forceinline__ int64_t chunk_of_wave() {
   return int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
 }
 
-__global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch P) {
+template <int N>
+__global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch<N> P) {
   const int64_t q = chunk_of_wave();
   if (q >= P.a.n_chunks) return;
   const GroupChunkDev ch = P.a.chunks[q];
@@ -121,9 +122,19 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
   const int64_t q = P.q_end - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
   const GroupChunkDev ch = P.chunks[q];
   const void* g = P.chunk_grads[q];
-  if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
-  if (g == nullptr) return;               // left out of this step
-  const StepScalars k = step_scalars(P.k, P.scalars, (ch.flags & kChunkDecayed) != 0);
+  double norm;
+  bool finite;
+  if (SPLIT && P.n_partials > 0) {
+    const double t = block_sum(int(threadIdx.x) < P.n_partials ? P.partials[threadIdx.x] : 0.0);
+    norm = sqrt(t);
+    finite = __builtin_isfinite(t);
+  } else {
+    norm = P.scalars[kNorm];
+    finite = P.scalars[kFinite] != 0.0;
+  }
+  if (!finite) return;        // non-finite norm: skip the step
+  if (g == nullptr) return;   // left out of this step
+  const StepScalars k = step_scalars(P.k, norm, (ch.flags & kChunkDecayed) != 0);
   StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
   if (SPLIT) {
     take_part<In, CODED>(c, int(blockIdx.x & 3));
@@ -136,6 +147,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
 
 template <typename In, bool CODED>
 void group_step(const GroupStepLaunch& a, hipStream_t s) {
+  static_assert(kFoldChunks <= kSplitChunks && kFoldChunks <= kBlock, "one partial per lane, split launches");
   const int64_t n = a.q_end - a.q_begin;
   if (n <= kSplitChunks)
     hipLaunchKernelGGL((k_group_adamw<In, CODED, true>), dim3(unsigned(4 * n)), dim3(kBlock), 0, s, a);
@@ -151,11 +163,14 @@ hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_group_norm(const GroupNormLaunch& a, hipStream_t s) {
+template <int N>
+hipError_t launch_group_norm(const GroupNormLaunch<N>& a, hipStream_t s) {
   if (a.a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_norm, dim3(unsigned((a.a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
+  hipLaunchKernelGGL(k_group_norm<N>, dim3(unsigned((a.a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
+template hipError_t launch_group_norm(const GroupNormLaunch<kGroupPointersShort>&, hipStream_t);
+template hipError_t launch_group_norm(const GroupNormLaunch<kGroupPointers>&, hipStream_t);
 
 hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s) {
   if (a.n_chunks <= 0) return hipSuccess;

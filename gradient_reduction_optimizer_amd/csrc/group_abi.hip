@@ -14,6 +14,9 @@ using namespace gro;
 
 namespace {
 
+// Whether the norm's second stage is left to the step's workgroups.
+bool folded(const gro_group* g) { return g->n_chunks <= kFoldChunks; }
+
 // A kind's number, 0..3: gradient type and moment type.
 int kind_of(uint32_t flags) { return ((flags & GRO_FP32_GRAD) ? 2 : 0) + ((flags & GRO_CODED_MOMENTS) ? 1 : 0); }
 
@@ -35,6 +38,16 @@ const GroupChunkDev* dev_chunks(const gro_group* g) {
 const void** dev_table(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->table_off); }
 const void** dev_grads(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->grad_off); }
 double* dev_partials(const gro_group* g) { return reinterpret_cast<double*>(g->d_ws + g->partial_off); }
+
+hipError_t launch_final(const gro_group* g, hipStream_t s) {
+  NormFinalLaunch f;
+  f.partials = dev_partials(g);
+  f.n_chunks = g->n_chunks;
+  f.group_sums = reinterpret_cast<double*>(g->d_ws + g->group_off);
+  f.counter = reinterpret_cast<uint32_t*>(g->d_ws + g->counter_off);
+  f.scalars = dev_scalars(g);
+  return launch_norm_final(f, s);
+}
 
 int64_t chunks_of(int64_t numel) { return (numel + kChunkElems - 1) / kChunkElems; }
 
@@ -233,14 +246,18 @@ extern "C" int gro_group_norm(gro_group* g, const void* const* d_grads, int32_t 
     for (int32_t i = 0; i < count; ++i) to[i] = d_grads[g->entries[size_t(first + i)].given];
   };
   hipError_t e = hipSuccess;
-  if (n <= kGroupPointers) {
-    GroupNormLaunch l;
-    std::memset(&l, 0, sizeof(l));
+  if (n <= kGroupPointersShort) {
+    GroupNormLaunch<kGroupPointersShort> l = {};
+    l.a = a;
+    copy(l.grads, 0, n);
+    e = launch_group_norm(l, s);
+  } else if (n <= kGroupPointers) {
+    GroupNormLaunch<kGroupPointers> l = {};
     l.a = a;
     copy(l.grads, 0, n);
     e = launch_group_norm(l, s);
   } else {
-    GroupTableLaunch l;
+    GroupTableLaunch l = {};
     l.table = dev_table(g);
     for (int32_t t = 0; t < n && e == hipSuccess; t += kGroupPointers) {
       l.t_first = t;
@@ -251,14 +268,10 @@ extern "C" int gro_group_norm(gro_group* g, const void* const* d_grads, int32_t 
     if (e == hipSuccess) e = launch_group_norm_table(a, s);
   }
   if (e != hipSuccess) return hip_fail(e, "group norm launch");
-  NormFinalLaunch f;
-  f.partials = dev_partials(g);
-  f.n_chunks = g->n_chunks;
-  f.group_sums = reinterpret_cast<double*>(g->d_ws + g->group_off);
-  f.counter = reinterpret_cast<uint32_t*>(g->d_ws + g->counter_off);
-  f.scalars = dev_scalars(g);
-  e = launch_norm_final(f, s);
-  if (e != hipSuccess) return hip_fail(e, "group norm stage-2 launch");
+  if (!folded(g)) {
+    e = launch_final(g, s);
+    if (e != hipSuccess) return hip_fail(e, "group norm stage-2 launch");
+  }
   g->norm_done = true;
   g->norm_valid = true;
   g->window = window_size;
@@ -278,6 +291,8 @@ extern "C" int gro_group_clip_adamw(gro_group* g, double max_norm, const gro_ada
   a.chunks = dev_chunks(g);
   a.chunk_grads = dev_grads(g);
   a.scalars = dev_scalars(g);
+  a.partials = dev_partials(g);
+  a.n_partials = folded(g) ? int32_t(g->n_chunks) : 0;
   a.k = adamw_consts(*hp, step, max_norm, g->window);
   for (int kind = 0; kind < 4; ++kind) {
     a.q_begin = g->kind_chunk[kind];
@@ -295,7 +310,9 @@ extern "C" int gro_group_get_norm(gro_group* g, double* norm, double* norm_sq, i
   if (rc != GRO_OK) return rc;
   if (!g->norm_valid) return set_error(GRO_E_STATE, "no gro_group_norm since the group was bound");
   double host[kNumScalars];
-  hipError_t e = hipStreamSynchronize(static_cast<hipStream_t>(g->norm_stream));
+  hipStream_t s = static_cast<hipStream_t>(g->norm_stream);
+  hipError_t e = folded(g) ? launch_final(g, s) : hipSuccess;
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
   if (e == hipSuccess) e = hipMemcpy(host, dev_scalars(g), sizeof(host), hipMemcpyDeviceToHost);
   if (e != hipSuccess) return hip_fail(e, "reading the norm");
   if (norm) *norm = host[kNorm];

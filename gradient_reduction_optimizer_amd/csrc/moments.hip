@@ -12,7 +12,7 @@ __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P)
   const int64_t q = P.n_chunks - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
   const ChunkDev ch = P.chunks[q];
   if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
-  const StepScalars k = step_scalars(P.k, P.scalars, P.buckets[ch.bucket].decayed != 0);
+  const StepScalars k = step_scalars(P.k, P.scalars[kNorm], P.buckets[ch.bucket].decayed != 0);
   const int64_t b = ch.begin / kCodedBlock;
   StepChunk c = {P.acc + ch.begin, P.master + ch.begin, P.moments.m + ch.begin, P.moments.v + ch.begin,
                  P.moments.m_scale + b, P.moments.v_scale + b,

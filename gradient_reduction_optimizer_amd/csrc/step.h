@@ -14,13 +14,13 @@ struct StepScalars : AdamScalars {
   float inv_sbc2;      // 1 / sbc2 rounded to nearest
 };
 
-// The step's scalars with the clip coefficient of the norm on the device.
-__device__ __forceinline__ StepScalars step_scalars(const AdamWConsts& c, const double* scalars, bool decayed) {
+// The step's scalars with the clip coefficient of the norm.
+__device__ __forceinline__ StepScalars step_scalars(const AdamWConsts& c, double norm, bool decayed) {
   StepScalars k;
   k.wdiv = make_divisor(c.window);
   k.coef = 1.0f;
   if (c.clip_on) {
-    const double r = c.max_norm / (scalars[kNorm] + 1e-6);
+    const double r = c.max_norm / (norm + 1e-6);
     k.coef = float(r < 1.0 ? r : 1.0);
   }
   k.decay = decayed ? c.decay : 1.0f;

@@ -189,6 +189,58 @@ def test_many_tensors(count):
     assert case.arena.guards_untouched()
 
 
+@pytest.mark.parametrize("chunks", [127, 128, 129, 512, 513])
+def test_sizes_around_the_launch_rules(chunks):
+    """Numbers of chunks where the launches change (a step split four ways, the
+    norm's second stage left to the step), of one kind and of two."""
+    for parts in ([chunks * 4096 - 5], [(chunks - 1) * 4096, 1], [4096] * 3 + [(chunks - 4) * 4096 - 9, 70]):
+        case = Case(parts, [8 if i % 2 == 0 else 32 for i in range(len(parts))], [BF16] * len(parts), seed=chunks)
+        assert case.group.info["n_chunks"] == chunks
+        before = case.state()
+        grads = case.gradients()
+        case.group.norm(grads, 1)
+        norm = case.group.get_norm()[0]
+        case.group.clip_adamw(0.5, HP, 2)
+        torch.cuda.synchronize()
+        check_step(case, before, grads, 1, 0.5, 2, norm, exact=False)
+        assert case.group.get_norm()[0] == norm    # still there after the step
+
+
+def test_a_captured_norm_with_an_eager_step():
+    """The step takes the norm of the gradients that lay there last, whether
+    the norm ran eagerly or was replayed, and get_norm reads the same one."""
+    case = Case([5000, 300], [8, 32], [BF16, BF16])
+    grads = case.gradients()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        case.group.norm(grads, 1)
+    for k in range(3):
+        for x, y in zip(grads, case.gradients(sigma=10.0 ** -k)):
+            x.copy_(y)
+        if k == 1:
+            case.group.norm(case.gradients(), 1)   # another one in between
+            case.group.get_norm()
+            torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        before = case.state()
+        norm = case.group.get_norm()[0]
+        assert abs(norm - oracle_norm(grads, 1)) <= 64 * 2.0 ** -53 * norm
+        case.group.clip_adamw(0.5, HP, 2)
+        torch.cuda.synchronize()
+        check_step(case, before, grads, 1, 0.5, 2, norm)
+        case.group.norm(grads, 1)                  # the host's state for the next step
+
+
+@pytest.mark.parametrize("count", [64, 65])
+def test_tensors_around_the_short_argument_list(count):
+    case = Case([50 + i for i in range(count)], [8] * count, [BF16] * count, seed=count)
+    run(case, case.gradients(without=(count - 1,)), 1, 1.0, 1)
+    run(case, case.gradients(), 1, 1.0, 2)
+
+
 def test_the_norm_does_not_depend_on_alignment_and_repeats():
     """The same values at every element offset: the same bits, each time."""
     rng = np.random.default_rng(1)
