@@ -389,11 +389,10 @@ def gro_group_bind(group: int, tensors: Sequence[Sequence[int]], d_workspace: in
     """tensors: per tensor the pointers (master, m, v, m_scale, v_scale,
     param_bf16), 0 for those it has not."""
     n = gro_group_get_info(group)["n_tensors"]
-    if len(tensors) != n:
-        raise ValueError(f"gro_group_bind: {len(tensors)} tensors given, the group has {n}")
-    rows = (gro_group_tensor * max(n, 1))()
-    for i, t in enumerate(tensors):
-        rows[i] = gro_group_tensor(*[int(p) for p in t])
+    if len(tensors) != n or any(len(t) != len(gro_group_tensor._fields_) for t in tensors):
+        raise ValueError(f"gro_group_bind: {n} tensors of {len(gro_group_tensor._fields_)} pointers each are needed")
+    flat = array("Q", [p for t in tensors for p in t])
+    rows = (gro_group_tensor * n).from_buffer(flat) if n else None
     _check(load().gro_group_bind(group, rows, d_workspace, int(nbytes), stream))
 
 

@@ -57,9 +57,10 @@ class DeviceState:
     workspace for one plan, allocated with torch on ``device`` and bound.
     With ``static_workspace`` no workspace is allocated: the plan is bound
     to the library's own per-GPU workspace (gro_plan_bind_static).  With
-    ``coded_moments`` the moments are held in 8 bits: ``m`` and ``v`` are
-    code bytes, ``m_scale`` and ``v_scale`` the blocks' scales, and ``coded``
-    their four pointers, for gro_clip_adamw_coded."""
+    ``coded_moments`` the moments are held in 8 bits: ``m_code`` and
+    ``v_code`` are code bytes, ``m_scale`` and ``v_scale`` the blocks' scales,
+    ``coded`` their four pointers, for gro_clip_adamw_coded, and there are
+    no ``m`` and ``v``."""
 
     def __init__(self, plan: Plan, device="cuda", with_bf16: bool = True, stream=None,
                  static_workspace: bool = False, coded_moments: bool = False):
@@ -72,11 +73,12 @@ class DeviceState:
         self.master = torch.zeros(n, **f32)
         self.coded = None
         if coded_moments:
-            self.m = torch.zeros(n, dtype=torch.uint8, device=self.device)
-            self.v = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self.m = self.v = None
+            self.m_code = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self.v_code = torch.zeros(n, dtype=torch.uint8, device=self.device)
             self.m_scale = torch.zeros(-(-n // B.GRO_CODED_BLOCK), **f32)
             self.v_scale = torch.zeros(-(-n // B.GRO_CODED_BLOCK), **f32)
-            self.coded = tuple(t.data_ptr() for t in (self.m, self.v, self.m_scale, self.v_scale))
+            self.coded = tuple(t.data_ptr() for t in (self.m_code, self.v_code, self.m_scale, self.v_scale))
         else:
             self.m = torch.zeros(n, **f32)
             self.v = torch.zeros(n, **f32)
@@ -143,7 +145,7 @@ class DeviceState:
 
 
 def _check_array(what: str, t, dtype, numel: int, device) -> None:
-    if t.dtype != dtype or t.numel() != numel or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.numel() != numel or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor of {numel} elements on {device} is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
@@ -184,24 +186,26 @@ class TensorGroup:
         self.masters, self.copies, self.bits, self.grad_dtype = list(masters), copies, bits, grad_dtype
         self.states = []
         rows = []
+        kinds = {32: (torch.float32,) * 2, 8: (torch.uint8,) * 2 + (torch.float32,) * 2}
         for i, p in enumerate(masters):
             k = p.numel()
             _check_array(f"master {i}", p, torch.float32, k, self.device)
             if copies[i] is not None:
                 _check_array(f"params_bf16 {i}", copies[i], torch.bfloat16, k, self.device)
-            kinds = [torch.float32] * 2 if bits[i] == 32 else [torch.uint8] * 2 + [torch.float32] * 2
-            sizes = [k, k, -(-k // B.GRO_CODED_BLOCK), -(-k // B.GRO_CODED_BLOCK)][:len(kinds)]
+            dtypes = kinds[bits[i]]
+            blocks = -(-k // B.GRO_CODED_BLOCK)
+            sizes = (k, k, blocks, blocks)[:len(dtypes)]
             if states is None:
-                st = tuple(torch.zeros(s, dtype=d, device=self.device) for s, d in zip(sizes, kinds))
+                st = tuple(torch.zeros(s, dtype=d, device=self.device) for s, d in zip(sizes, dtypes))
             else:
                 st = tuple(states[i])
-                if len(st) != len(kinds):
-                    raise ValueError(f"states {i}: {len(kinds)} tensors are needed, got {len(st)}")
-                for t, s, d in zip(st, sizes, kinds):
+                if len(st) != len(dtypes):
+                    raise ValueError(f"states {i}: {len(dtypes)} tensors are needed, got {len(st)}")
+                for t, s, d in zip(st, sizes, dtypes):
                     _check_array(f"states {i}", t, d, s, self.device)
             self.states.append(st)
-            ptrs = [t.data_ptr() for t in st] + [0] * (4 - len(st))
-            rows.append([p.data_ptr(), *ptrs, 0 if copies[i] is None else copies[i].data_ptr()])
+            rows.append([p.data_ptr(), *[t.data_ptr() for t in st], *[0] * (4 - len(st)),
+                         0 if copies[i] is None else copies[i].data_ptr()])
         self.handle = B.gro_group_create([dict(numel=p.numel(), no_decay=bool(nd), coded_moments=b == 8,
                                                fp32_grad=gd == torch.float32)
                                           for p, nd, b, gd in zip(masters, no_decay, bits, grad_dtype)])

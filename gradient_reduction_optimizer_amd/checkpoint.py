@@ -71,6 +71,9 @@ def save_state(plan, master, m, v, step: int, directory: str) -> None:
     import torch
     from safetensors.torch import save_file
 
+    for name, arr in (("master", master), ("m", m), ("v", v)):
+        if arr is None or arr.dtype != torch.float32:
+            raise CheckpointError(f"{name}: flat FP32 arrays are saved (8-bit moments: save_device_state)")
     os.makedirs(directory, exist_ok=True)
     manifest = os.path.join(directory, MANIFEST)
     if os.path.exists(manifest):

@@ -37,7 +37,7 @@
  *  - Device pointers must be 16-byte aligned (256-byte for the workspace).
  *  - Streams: `stream` is a hipStream_t passed as void* (NULL = the null
  *    stream).  All device work is enqueued on it, asynchronously.  Use one
- *    stream per plan at a time.
+ *    stream per plan, or per group, at a time.
  *  - Errors: functions return GRO_OK (0) or a negative GRO_E_* code and set
  *    a thread-local message (gro_last_error).  Validation precedes any device
  *    work.  Non-finite data is reported through gro_plan_get_norm's `finite`

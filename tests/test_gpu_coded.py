@@ -57,11 +57,11 @@ class Side:
         self.gen.manual_seed(seed)
         self.nb = self.plan.info["n_buckets"]
         st = self.st
-        self.arrays = [st.acc, st.master, st.p_bf16, st.m, st.v, st.m_scale, st.v_scale]
+        self.arrays = [st.acc, st.master, st.p_bf16, st.m_code, st.v_code, st.m_scale, st.v_scale]
         for a in self.arrays:
             a.view(torch.uint8).fill_(POISON)
         for b in range(self.nb):
-            for a, scale in ((st.master, False), (st.m, False), (st.v, False), (st.m_scale, True), (st.v_scale, True)):
+            for a, scale in ((st.master, False), (st.m_code, False), (st.v_code, False), (st.m_scale, True), (st.v_scale, True)):
                 a[self.span(b, scale)] = 0
             s = self.span(b)
             st.master[s] = 0.02 * torch.randn(s.stop - s.start, generator=self.gen, device="cuda")
@@ -82,10 +82,10 @@ class Side:
 
     def coded(self, b):
         s, k = self.span(b), self.span(b, True)
-        return host(self.st.m[s]), host(self.st.v[s]), host(self.st.m_scale[k]), host(self.st.v_scale[k])
+        return host(self.st.m_code[s]), host(self.st.v_code[s]), host(self.st.m_scale[k]), host(self.st.v_scale[k])
 
     def state(self):
-        return [host(x) for x in (self.st.master, self.st.p_bf16, self.st.m, self.st.v, self.st.m_scale, self.st.v_scale)]
+        return [host(x) for x in (self.st.master, self.st.p_bf16, self.st.m_code, self.st.v_code, self.st.m_scale, self.st.v_scale)]
 
     def gradients(self, n, sigma=1e-2):
         """n microbatches of bucket buffers; NaN behind each bucket's end."""
@@ -383,6 +383,11 @@ def test_checkpoints_carry_8_bit_moments(tmp_path):
         a.window(a.gradients(1))
         a.update(1, 1.0, t)
     C.save_device_state(a.st, 2, str(tmp_path / "ck"))
+    assert a.st.m is None and a.st.v is None
+    with pytest.raises(C.CheckpointError):
+        C.save_state(a.plan, a.st.master, a.st.m_code, a.st.v_code, 2, str(tmp_path / "codes"))
+    with pytest.raises(C.CheckpointError):
+        C.save_state(a.plan, a.st.master, a.st.m, a.st.v, 2, str(tmp_path / "codes"))
     b = Side(tensors, 2, 1 << 20, seed=3)
     assert C.load_device_state(b.st, str(tmp_path / "ck")) == 2
     grads = a.gradients(1)
@@ -438,8 +443,8 @@ def test_offsets_past_32_bits():
         p, coded, bits = M.adamw_update_coded(vals[k][0], F32(1), vals[k][1], zero, sc, True)
         same_bits(host(st.master[e]), p, (k, "p"))
         same_bits(host(st.p_bf16[e]), bits, (k, "copy"))
-        same_bits(host(st.m[e]), coded[0], (k, "m"))
-        same_bits(host(st.v[e]), coded[1], (k, "v"))
+        same_bits(host(st.m_code[e]), coded[0], (k, "m"))
+        same_bits(host(st.v_code[e]), coded[1], (k, "v"))
         same_bits(host(m[e]), M.decode_m(coded[0], coded[2]), (k, "decoded m"))
         same_bits(host(v[e]), M.decode_v(coded[1], coded[3]), (k, "decoded v"))
-    assert not bool(st.m[10_000:20_000].any())
+    assert not bool(st.m_code[10_000:20_000].any())

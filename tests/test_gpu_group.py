@@ -53,13 +53,16 @@ class Case:
     """A group of the given sizes, its state before a step on the host, and
     what the oracle makes of it."""
 
-    def __init__(self, sizes, bits, dtypes, shift=0, seed=0, copies=True):
+    def __init__(self, sizes, bits, dtypes, shift=0, seed=0, copies=True, shift_of=None):
+        """shift: of every array, or per kind of array from shift_of (p, copy,
+        state, grad), which is 0 for those it does not name."""
         self.sizes, self.bits, self.dtypes = sizes, bits, dtypes
         self.rng = np.random.default_rng(seed)
         self.arena = Arena(shift)
-        cut = lambda a: self.arena.cut(torch.from_numpy(a).cuda())  # noqa: E731
-        self.p = [cut((self.rng.normal(size=n) * 0.02).astype(F32)) for n in sizes]
-        self.copy = [cut(np.zeros(n, np.int16)).view(BF16) if copies and i % 4 != 3 else None
+        self.shift_of = shift_of
+        cut = lambda a, kind="state": self.cut(torch.from_numpy(a).cuda(), kind)  # noqa: E731
+        self.p = [cut((self.rng.normal(size=n) * 0.02).astype(F32), "p") for n in sizes]
+        self.copy = [cut(np.zeros(n, np.int16), "copy").view(BF16) if copies and i % 4 != 3 else None
                      for i, n in enumerate(sizes)]
         self.states = []
         for n, b in zip(sizes, bits):
@@ -74,11 +77,16 @@ class Case:
         self.group = TensorGroup(self.p, state_bits=bits, no_decay=self.no_decay, grad_dtype=dtypes,
                                  params_bf16=self.copy, states=self.states)
 
+    def cut(self, values, kind):
+        if self.shift_of is not None:
+            self.arena.shift = self.shift_of.get(kind, 0)
+        return self.arena.cut(values)
+
     def gradients(self, sigma=1e-2, without=()):
         out = []
         for i, (n, d) in enumerate(zip(self.sizes, self.dtypes)):
             g = (self.rng.normal(size=n) * sigma * np.exp(self.rng.normal(size=n))).astype(F32)
-            out.append(None if i in without else self.arena.cut(torch.from_numpy(g).cuda().to(d)))
+            out.append(None if i in without else self.cut(torch.from_numpy(g).cuda().to(d), "grad"))
         return out
 
     def state(self):
@@ -149,6 +157,16 @@ def test_steps_match_the_oracle_and_64_bits(bits, dtype, shift):
     for step, (n, max_norm) in enumerate(((1, 1.0), (3, 0.02), (4, 0.0)), 1):
         run(case, case.gradients(), n, max_norm, step)
     assert case.arena.guards_untouched()
+
+
+@pytest.mark.parametrize("kind", ["p", "copy", "state", "grad"])
+def test_one_misaligned_array(kind):
+    """Only one of a tensor's arrays off its vector alignment."""
+    sizes = [4096, 4097, 70, 9000]
+    for bits, dtype in ((8, BF16), (32, FP32)):
+        case = Case(sizes, [bits] * 4, [dtype] * 4, seed=3, shift_of={kind: 1})
+        run(case, case.gradients(), 1, 1.0, 1)
+        assert case.arena.guards_untouched()
 
 
 def test_mixed_kinds_and_tensors_without_a_gradient():
