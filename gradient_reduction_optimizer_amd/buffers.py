@@ -221,7 +221,7 @@ class TensorGroup:
 
     def _stream(self, stream) -> int:
         import torch
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        return (torch.cuda.current_stream(self.device.index) if stream is None else stream).cuda_stream
 
     def close(self) -> None:
         if self.handle:
