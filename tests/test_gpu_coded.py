@@ -372,6 +372,32 @@ def test_two_plans_on_two_streams():
             same_bits(got, want, "state")
 
 
+def test_a_state_on_a_stream_of_its_own():
+    """Steps on the state's stream, moments read and set from the current one,
+    with nothing of the caller's between them."""
+    tensors = specs([3_000_000, 4096])
+    stream = torch.cuda.Stream()
+    plan = Plan(tensors, 2, 1 << 22)
+    st = DeviceState(plan, "cuda", stream=stream, coded_moments=True)
+    ref = DeviceState(Plan(tensors, 2, 1 << 22), "cuda", coded_moments=True)
+    grads = [torch.randn(b.shape, device="cuda").to(b.dtype) for b in st.grad_buffers()]
+    ones = torch.ones_like(st.master)
+    torch.cuda.synchronize()
+    found = []
+    for state, s in ((st, stream), (ref, torch.cuda.current_stream())):
+        h, nb, acc = state.plan.handle, plan.info["n_buckets"], state.acc.data_ptr()
+        for step in range(1, 6):
+            B.gro_accumulate_window(h, 0, nb, [g.data_ptr() for g in grads], 1, acc, s.cuda_stream)
+            B.gro_reduce_norm(h, acc, 1, s.cuda_stream)
+            B.gro_clip_adamw_coded(h, acc, 1, 1.0, HP, step, state.master.data_ptr(), state.coded,
+                                   state.p_bf16.data_ptr(), s.cuda_stream)
+            if step == 2:
+                state.set_moments(ones * 1e-3, ones * 1e-6)
+        found.append([host(x) for x in (*state.moments(), state.master)])
+    for got, want in zip(*found):
+        same_bits(got, want, "stream")
+
+
 def test_checkpoints_carry_8_bit_moments(tmp_path):
     """Saved after two steps and restored into a fresh state of the same
     layout, the third step is the uninterrupted run's bit for bit; restored
