@@ -1,6 +1,12 @@
 // gfx950 kernels on a plan whose Adam moments are held in 8 bits: clip + AdamW,
 // and the moments' conversion from and to FP32.  The format is in coded.h, one
 // chunk's step in step.h; the walk over the chunk table is that of kernels.hip.
+//
+// Bound by HBM: clip + AdamW moves 1.23 GB for 67M elements in 182 us (6.7
+// TB/s, part of the accumulator still in the Infinity Cache) and 2.72 GB for
+// 167M without a copy in 450 us (6.0 TB/s); encoding 167M elements moves 1.69
+// GB in 273 us (6.2 TB/s), decoding 67M 680 MB in 114 us (6.0 TB/s).  Sets of
+// one or two chunks per CU wait on latency: 2.4 to 4.5 us.
 #include "step.h"
 
 namespace gro {

@@ -2,6 +2,14 @@
 // device side.  A lane owns 4-element vectors lane, lane + kBlock, ... of its
 // chunk, as in every pass, so with 8-bit moments a block of 64 elements is
 // one row of 16 lanes (see coded.h).
+//
+//   g^ = g / window * coef;  m = b1 m + (1-b1) g^;  v = b2 v + (1-b2) g^^2
+//   p = p decay - step_size m / (sqrt(v) / sbc2 + eps)
+//
+// All of it is one pass over memory: 18.25 bytes an element with 8-bit moments
+// and a BF16 copy on an FP32 accumulator, 28 with FP32 moments on BF16
+// gradients.  Four vectors per lane in flight measured best: an 8-bit step of
+// 167M elements 446 us against 477 with two and 480 with one.
 #pragma once
 
 #include "coded.h"
@@ -37,7 +45,7 @@ __device__ __forceinline__ StepScalars step_scalars(const AdamWConsts& c, double
 
 // r = sqrt(v) and q = r / sbc2, both rounded to nearest as the IEEE operations
 // round.  For v from 2^-96 to the largest finite value, which is every v of a
-// vector but in odd cases, with fewer issue slots (18 instead of 32):
+// vector but in odd cases, with fewer issue slots (about 15 instead of 31):
 //   r: the hardware reciprocal root y, g = v y, r = g + (v - g^2) y/2.  Equal to
 //      the IEEE root for every FP32 in that range (all of them compared on a
 //      gfx950); below, v - g^2 would round.
