@@ -153,7 +153,7 @@ def load() -> ctypes.CDLL:
     L.gro_group_destroy.restype = None
     L.gro_group_get_info.argtypes = [P, ctypes.POINTER(gro_group_info)]
     L.gro_group_bind.argtypes = [P, ctypes.POINTER(gro_group_tensor), P, U64, P]
-    L.gro_group_norm.argtypes = [P, ctypes.POINTER(P), I32, P]
+    L.gro_group_norm.argtypes = [P, P, I32, P]
     L.gro_group_clip_adamw.argtypes = [P, D, ctypes.POINTER(gro_adamw_hparams), I64, P]
     L.gro_group_get_norm.argtypes = [P, ctypes.POINTER(D), ctypes.POINTER(D), ctypes.POINTER(I32)]
     L.gro_last_error.argtypes = []
@@ -405,8 +405,7 @@ def gro_group_norm(group: int, d_grads: Sequence[int], window_size: int = 1, str
     if len(d_grads) != n:
         raise ValueError(f"gro_group_norm: {len(d_grads)} pointers given, the call reads {n}")
     flat = array("Q", d_grads)  # a group has thousands of tensors: one conversion of the whole list
-    ptrs = (ctypes.c_void_p * n).from_buffer(flat) if n else None
-    _check(load().gro_group_norm(group, ptrs, int(window_size), stream))
+    _check(load().gro_group_norm(group, flat.buffer_info()[0], int(window_size), stream))
 
 
 def gro_group_clip_adamw(group: int, max_norm: float, hp: dict, step: int, stream: int = 0) -> None:

@@ -7,6 +7,8 @@
 // 167M without a copy in 450 us (6.0 TB/s); encoding 167M elements moves 1.69
 // GB in 273 us (6.2 TB/s), decoding 67M 680 MB in 114 us (6.0 TB/s).  Sets of
 // one or two chunks per CU wait on latency: 2.4 to 4.5 us.
+#include <algorithm>
+
 #include "step.h"
 
 namespace gro {
@@ -132,18 +134,35 @@ hipError_t launch_adamw_coded(const CodedStepLaunch& a, bool acc_nt, hipStream_t
   return hipGetLastError();
 }
 
-hipError_t launch_moments_encode(const MomentsLaunch& a, hipStream_t s) {
-  if (a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_moments_encode<kEncodeVecs>, dim3(unsigned(a.n_chunks * (kVecsPerLane / kEncodeVecs))), dim3(kBlock), 0, s,
-                     a);
-  return hipGetLastError();
+// A launch has fewer than 2^32 lanes: with up to four workgroups per chunk, 2^21
+// chunks (8.6e9 elements) at a time.
+constexpr int64_t kMomentsSlice = int64_t(1) << 21;
+static_assert(kMomentsSlice * kVecsPerLane * kBlock < (int64_t(1) << 32), "one launch's lanes");
+
+template <typename Launch>
+hipError_t in_slices(MomentsLaunch a, Launch launch) {
+  hipError_t e = hipSuccess;
+  for (int64_t left = a.n_chunks; left > 0 && e == hipSuccess; left -= kMomentsSlice) {
+    a.n_chunks = std::min(left, kMomentsSlice);
+    launch(a);
+    e = hipGetLastError();
+    a.chunks += a.n_chunks;
+  }
+  return e;
 }
 
-hipError_t launch_moments_decode(const MomentsLaunch& a, hipStream_t s) {
-  if (a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_moments_decode<kDecodeVecs>, dim3(unsigned(a.n_chunks * (kVecsPerLane / kDecodeVecs))), dim3(kBlock), 0, s,
-                     a);
-  return hipGetLastError();
+hipError_t launch_moments_encode(const MomentsLaunch& args, hipStream_t s) {
+  return in_slices(args, [s](const MomentsLaunch& a) {
+    const dim3 grid(unsigned(a.n_chunks * (kVecsPerLane / kEncodeVecs)));
+    hipLaunchKernelGGL(k_moments_encode<kEncodeVecs>, grid, dim3(kBlock), 0, s, a);
+  });
+}
+
+hipError_t launch_moments_decode(const MomentsLaunch& args, hipStream_t s) {
+  return in_slices(args, [s](const MomentsLaunch& a) {
+    const dim3 grid(unsigned(a.n_chunks * (kVecsPerLane / kDecodeVecs)));
+    hipLaunchKernelGGL(k_moments_decode<kDecodeVecs>, grid, dim3(kBlock), 0, s, a);
+  });
 }
 
 }  // namespace gro

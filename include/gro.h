@@ -67,7 +67,7 @@ extern "C" {
 #define GRO_OK            0
 #define GRO_E_INVALID    (-1)  /* null/misaligned pointer, bad size/shape/step/window, NaN max_norm */
 #define GRO_E_PLACEMENT  (-2)  /* unknown placement, shard_index out of range, bad flags */
-#define GRO_E_DUPLICATE  (-3)  /* a second owner for one param_id */
+#define GRO_E_DUPLICATE  (-3)  /* a second owner for one param_id, or for memory of a group */
 #define GRO_E_STATE      (-4)  /* unbound plan, window bookkeeping violated */
 #define GRO_E_HIP        (-5)  /* HIP runtime or launch error */
 

@@ -332,7 +332,8 @@ def decode_m(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
     v = np.append(e4m3_values(), np.nan)[codes & 127].astype(F32)
     v = np.where(codes >= 128, -v, v)
     k = np.asarray(scales, dtype=F32) * F32(1 / 256)
-    return v * np.repeat(k, CODED_BLOCK)[:codes.size]
+    with np.errstate(invalid="ignore"):
+        return v * np.repeat(k, CODED_BLOCK)[:codes.size]
 
 
 def encode_v(v: np.ndarray):

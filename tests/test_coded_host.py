@@ -115,6 +115,60 @@ def test_edges_of_the_formats():
         assert np.isnan(d[:64]).all() and np.array_equal(d[64:], m[64:])
 
 
+# Plausible mistakes in the formats, each of which a check above has to see.
+def _truncated(y, values):
+    return np.clip(np.searchsorted(values, np.asarray(y, np.float64), side="right") - 1, 0, len(values) - 1)
+
+
+def _ties_up(y, values):
+    y = np.asarray(y, np.float64)
+    lo = _truncated(y, values).clip(0, len(values) - 2)
+    return np.where(y - values[lo] >= values[lo + 1] - y, lo + 1, lo)
+
+
+def _no_gradual_underflow():
+    c = np.arange(256)
+    return np.where(c == 0, 0.0, (1.0 + (c & 15) / 16.0) * 2.0 ** ((c >> 4) - 15.0))
+
+
+def _codes_that_may_vanish(v, encode=M.encode_v):
+    codes, s = encode(v)
+    r = np.sqrt(np.asarray(v, np.float64))
+    y = r / np.where(s == 0, 1, s).repeat(64)[:r.size]
+    return np.where(y < 2.0 ** -19, 0, codes).astype(np.uint8), s
+
+
+def _scale_of_v(v, encode=M.encode_v):
+    codes, s = encode(v)
+    return codes, (s * s).astype(F32)
+
+
+def _scale_to_the_next_power_of_two(m, encode=M.encode_m):
+    codes, s = encode(m)
+    up = np.where(s > 0, 2.0 ** np.ceil(np.log2(np.where(s > 0, s, 1))), 0).astype(F32)
+    return codes, up
+
+
+MISTAKES = [("nearest_code", _truncated), ("nearest_code", _ties_up), ("root_values", _no_gradual_underflow),
+            ("encode_v", _codes_that_may_vanish), ("encode_v", _scale_of_v),
+            ("encode_m", _scale_to_the_next_power_of_two)]
+
+
+@pytest.mark.parametrize("name,wrong", MISTAKES, ids=[w.__name__ for _, w in MISTAKES])
+def test_mistakes_in_the_formats_are_seen(monkeypatch, name, wrong):
+    monkeypatch.setattr(M, name, wrong)
+    checks = [test_e4m3_table_is_torchs, test_root_codes_are_bits_6_to_13_of_fp16, test_edges_of_the_formats,
+              lambda: test_oracle_encodes_to_the_nearest_code("wide", 4099),
+              lambda: test_encoding_what_was_decoded_changes_nothing("plain")]
+    seen = 0
+    for check in checks:
+        try:
+            check()
+        except AssertionError:
+            seen += 1
+    assert seen > 0
+
+
 # ---------------------------------------------------------------- the host
 def code_of(fn):
     with pytest.raises(B.GroError) as e:

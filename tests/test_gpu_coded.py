@@ -474,3 +474,49 @@ def test_offsets_past_32_bits():
         same_bits(host(m[e]), M.decode_m(coded[0], coded[2]), (k, "decoded m"))
         same_bits(host(v[e]), M.decode_v(coded[1], coded[3]), (k, "decoded v"))
     assert not bool(st.m_code[10_000:20_000].any())
+
+
+def test_conversions_of_more_chunks_than_one_launch_takes():
+    """Past 2^21 chunks a conversion is several launches: codes on both sides
+    of the seam, decoded and encoded again."""
+    n = (1 << 33) + 4096 * 3 + 5
+    need = n * 10 + n // 8 + (1 << 30)
+    if torch.cuda.mem_get_info()[0] < need + (16 << 30):
+        pytest.skip("needs 102 GB of free device memory")
+    plan = Plan([dict(param_id=0, shape=(n,), placement="reduced")], 1, 1 << 40)
+    assert plan.info["n_chunks"] > 1 << 21
+    ws = torch.empty(plan.info["workspace_bytes"] + 256, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    B.gro_plan_bind(plan.handle, (ws.data_ptr() + 255) // 256 * 256, plan.info["workspace_bytes"], s)
+    flat = plan.info["n_flat"]
+    codes = [torch.zeros(flat, dtype=torch.uint8, device="cuda") for _ in "mv"]
+    scales = [torch.zeros(flat // 64, device="cuda") for _ in "mv"]
+    state = tuple(t.data_ptr() for t in codes + scales)
+    rng = np.random.default_rng(0)
+    spots = [slice(0, 4096), slice((1 << 33) - 4096, (1 << 33) + 8192), slice(n - 4096 - 5, n)]
+    want = []
+    for sp in spots:
+        x = (rng.normal(size=sp.stop - sp.start) * np.exp(rng.normal(size=sp.stop - sp.start))).astype(F32)
+        want.append((M.encode_m(x), M.encode_v(x * x)))
+    m, v = (torch.zeros(flat, device="cuda") for _ in "mv")
+    try:
+        for sp, ((mc, ms), (vc, vs)) in zip(spots, want):
+            m[sp] = torch.from_numpy(M.decode_m(mc, ms)).cuda()
+            v[sp] = torch.from_numpy(M.decode_v(vc, vs)).cuda()
+        B.gro_moments_encode(plan.handle, m.data_ptr(), v.data_ptr(), state, s)
+        m.fill_(7.0)
+        v.fill_(7.0)
+        B.gro_moments_decode(plan.handle, state, m.data_ptr(), v.data_ptr(), s)
+        torch.cuda.synchronize()
+        for sp, ((mc, ms), (vc, vs)) in zip(spots, want):
+            blocks = slice(sp.start // 64, -(-sp.stop // 64))
+            same_bits(host(codes[0][sp]), mc, "m")
+            same_bits(host(codes[1][sp]), vc, "v")
+            same_bits(host(scales[0][blocks]), ms, "m_scale")
+            same_bits(host(scales[1][blocks]), vs, "v_scale")
+            same_bits(host(m[sp]), M.decode_m(mc, ms), "decoded m")
+            same_bits(host(v[sp]), M.decode_v(vc, vs), "decoded v")
+        assert not bool(m[(1 << 33) + 8192:n - 4096 - 5].any()) and not bool(codes[1][4096:1 << 20].any())
+    finally:
+        del m, v, codes, scales
+        torch.cuda.empty_cache()
