@@ -36,21 +36,13 @@ enum GroupChunkFlag : uint16_t {
   kChunkWide = 4,          // the arrays above take four-element accesses
 };
 
-// Writes n tensors' gradient pointers into the table, from tensor t_first on.
-struct GroupTableLaunch {
-  const void** table;
-  int32_t t_first;
-  int32_t n;
-  const void* grads[kGroupPointers];
-};
-
 struct GroupNormArgs {
   const GroupChunkDev* chunks;
-  int64_t n_chunks;
-  const void* const* table;   // every tensor's gradient, when not in `grads`
+  int64_t q_begin, q_end;
   const void** chunk_grads;   // out: every chunk's gradient, for the step
   double* partials;
   int32_t window;
+  int32_t t_first;            // tensor of grads[0]
 };
 template <int N>
 struct GroupNormLaunch {
@@ -77,11 +69,8 @@ struct GroupStepLaunch {
 // numbers at most.
 constexpr int64_t kFoldChunks = 128;
 
-hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s);
-// With the gradients of all tensors in the arguments, or in the table.
 template <int N>
 hipError_t launch_group_norm(const GroupNormLaunch<N>& a, hipStream_t s);
-hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s);
 // The chunks of [q_begin, q_end) all have gradients of one type and moments
 // of one kind.
 hipError_t launch_group_step(const GroupStepLaunch& a, bool fp32, bool coded, hipStream_t s);
@@ -97,11 +86,12 @@ struct gro_group {
     int32_t given;         // index as given
     uint32_t flags;
     int64_t numel;
+    int64_t first_chunk;
   };
   std::vector<Entry> entries;
   int64_t n_chunks = 0;
   int64_t kind_chunk[5] = {0, 0, 0, 0, 0};  // first chunk of each kind, and the end
-  uint64_t scalar_off = 0, table_off = 0, chunk_off = 0, grad_off = 0, partial_off = 0, group_off = 0,
+  uint64_t scalar_off = 0, chunk_off = 0, grad_off = 0, partial_off = 0, group_off = 0,
            counter_off = 0, counter_bytes = 0, total = 0;
 
   char* d_ws = nullptr;

@@ -94,29 +94,14 @@ __device__ void norm_chunk(const GroupNormArgs& P, int64_t q, const GroupChunkDe
   }
 }
 
-// Chunk of this wave; the wave's number is the same in all of its lanes.
-__device__ __forceinline__ int64_t chunk_of_wave() {
-  return int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-}
-
 template <int N>
 __global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch<N> P) {
-  const int64_t q = chunk_of_wave();
-  if (q >= P.a.n_chunks) return;
+  // Chunk of this wave; the wave's number is the same in all of its lanes.
+  const int64_t q =
+      P.a.q_begin + int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  if (q >= P.a.q_end) return;
   const GroupChunkDev ch = P.a.chunks[q];
-  norm_chunk(P.a, q, ch, P.grads[ch.tensor]);
-}
-
-__global__ __launch_bounds__(kBlock) void k_group_norm_table(const GroupNormArgs P) {
-  const int64_t q = chunk_of_wave();
-  if (q >= P.n_chunks) return;
-  const GroupChunkDev ch = P.chunks[q];
-  norm_chunk(P, q, ch, P.table[ch.tensor]);
-}
-
-__global__ __launch_bounds__(kBlock) void k_group_table(const GroupTableLaunch P) {
-  const int i = int(blockIdx.x) * kBlock + int(threadIdx.x);
-  if (i < P.n) P.table[P.t_first + i] = P.grads[i];
+  norm_chunk(P.a, q, ch, P.grads[ch.tensor - P.a.t_first]);
 }
 
 // At least 4 waves per SIMD (at most 128 registers): the path of cut-off chunks
@@ -162,26 +147,15 @@ void group_step(const GroupStepLaunch& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_group_table(const GroupTableLaunch& a, hipStream_t s) {
-  if (a.n <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_table, dim3(unsigned((a.n + kBlock - 1) / kBlock)), dim3(kBlock), 0, s, a);
-  return hipGetLastError();
-}
-
 template <int N>
 hipError_t launch_group_norm(const GroupNormLaunch<N>& a, hipStream_t s) {
-  if (a.a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_norm<N>, dim3(unsigned((a.a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
+  const int64_t n = a.a.q_end - a.a.q_begin;
+  if (n <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_group_norm<N>, dim3(unsigned((n + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
   return hipGetLastError();
 }
 template hipError_t launch_group_norm(const GroupNormLaunch<kGroupPointersShort>&, hipStream_t);
 template hipError_t launch_group_norm(const GroupNormLaunch<kGroupPointers>&, hipStream_t);
-
-hipError_t launch_group_norm_table(const GroupNormArgs& a, hipStream_t s) {
-  if (a.n_chunks <= 0) return hipSuccess;
-  hipLaunchKernelGGL(k_group_norm_table, dim3(unsigned((a.n_chunks + kWaves - 1) / kWaves)), dim3(kBlock), 0, s, a);
-  return hipGetLastError();
-}
 
 hipError_t launch_group_step(const GroupStepLaunch& a, bool fp32, bool coded, hipStream_t s) {
   if (a.q_end <= a.q_begin) return hipSuccess;

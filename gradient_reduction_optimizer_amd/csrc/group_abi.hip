@@ -35,7 +35,6 @@ double* dev_scalars(const gro_group* g) { return reinterpret_cast<double*>(g->d_
 const GroupChunkDev* dev_chunks(const gro_group* g) {
   return reinterpret_cast<const GroupChunkDev*>(g->d_ws + g->chunk_off);
 }
-const void** dev_table(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->table_off); }
 const void** dev_grads(const gro_group* g) { return reinterpret_cast<const void**>(g->d_ws + g->grad_off); }
 double* dev_partials(const gro_group* g) { return reinterpret_cast<double*>(g->d_ws + g->partial_off); }
 
@@ -47,6 +46,24 @@ hipError_t launch_final(const gro_group* g, hipStream_t s) {
   f.counter = reinterpret_cast<uint32_t*>(g->d_ws + g->counter_off);
   f.scalars = dev_scalars(g);
   return launch_norm_final(f, s);
+}
+
+// The norm's first stage, N tensors' gradient pointers to a launch.
+template <int N>
+hipError_t launch_norms(const gro_group* g, const GroupNormArgs& args, const void* const* d_grads, hipStream_t s) {
+  const int32_t n = int32_t(g->entries.size());
+  hipError_t e = hipSuccess;
+  for (int32_t t = 0; t < n && e == hipSuccess; t += N) {
+    const int32_t te = std::min(n, t + N);
+    GroupNormLaunch<N> l = {};
+    l.a = args;
+    l.a.q_begin = g->entries[size_t(t)].first_chunk;
+    l.a.q_end = te < n ? g->entries[size_t(te)].first_chunk : g->n_chunks;
+    l.a.t_first = t;
+    for (int32_t i = t; i < te; ++i) l.grads[i - t] = d_grads[g->entries[size_t(i)].given];
+    e = launch_group_norm(l, s);
+  }
+  return e;
 }
 
 int64_t chunks_of(int64_t numel) { return (numel + kChunkElems - 1) / kChunkElems; }
@@ -71,7 +88,7 @@ int fill_group(gro_group* g, const gro_group_desc* tensors, int32_t n) {
     for (int32_t i = 0; i < n; ++i) {
       const gro_group_desc& d = tensors[i];
       if (d.numel == 0 || kind_of(d.flags) != kind) continue;
-      g->entries.push_back(gro_group::Entry{i, d.flags, d.numel});
+      g->entries.push_back(gro_group::Entry{i, d.flags, d.numel, q});
       q += chunks_of(d.numel);
     }
   }
@@ -85,7 +102,6 @@ int fill_group(gro_group* g, const gro_group_desc* tensors, int32_t n) {
   };
   const uint64_t chunks = uint64_t(g->n_chunks);
   g->scalar_off = place(256);
-  g->table_off = place(g->entries.size() * sizeof(void*));
   g->chunk_off = place(chunks * sizeof(GroupChunkDev));
   g->grad_off = place(chunks * sizeof(void*));
   g->partial_off = place(chunks * sizeof(double));
@@ -236,37 +252,13 @@ extern "C" int gro_group_norm(gro_group* g, const void* const* d_grads, int32_t 
   g->norm_done = false;  // from here on the pointers of an earlier call are being replaced
   GroupNormArgs a;
   a.chunks = dev_chunks(g);
-  a.n_chunks = g->n_chunks;
-  a.table = dev_table(g);
   a.chunk_grads = dev_grads(g);
   a.partials = dev_partials(g);
   a.window = window_size;
   const int32_t n = int32_t(g->entries.size());
-  const auto copy = [&](const void** to, int32_t first, int32_t count) {
-    for (int32_t i = 0; i < count; ++i) to[i] = d_grads[g->entries[size_t(first + i)].given];
-  };
   hipError_t e = hipSuccess;
-  if (n <= kGroupPointersShort) {
-    GroupNormLaunch<kGroupPointersShort> l = {};
-    l.a = a;
-    copy(l.grads, 0, n);
-    e = launch_group_norm(l, s);
-  } else if (n <= kGroupPointers) {
-    GroupNormLaunch<kGroupPointers> l = {};
-    l.a = a;
-    copy(l.grads, 0, n);
-    e = launch_group_norm(l, s);
-  } else {
-    GroupTableLaunch l = {};
-    l.table = dev_table(g);
-    for (int32_t t = 0; t < n && e == hipSuccess; t += kGroupPointers) {
-      l.t_first = t;
-      l.n = std::min(n - t, int32_t(kGroupPointers));
-      copy(l.grads, t, l.n);
-      e = launch_group_table(l, s);
-    }
-    if (e == hipSuccess) e = launch_group_norm_table(a, s);
-  }
+  if (n <= kGroupPointersShort) e = launch_norms<kGroupPointersShort>(g, a, d_grads, s);
+  else e = launch_norms<kGroupPointers>(g, a, d_grads, s);
   if (e != hipSuccess) return hip_fail(e, "group norm launch");
   if (!folded(g)) {
     e = launch_final(g, s);

@@ -33,7 +33,7 @@ import sys
 from collections import defaultdict
 
 OURS = ("k_accumulate_window", "k_accumulate", "k_adamw_coded", "k_adamw", "k_norm_partials", "k_norm_final",
-        "k_moments_encode", "k_moments_decode", "k_group_norm_table", "k_group_norm", "k_group_table", "k_group_adamw")
+        "k_moments_encode", "k_moments_decode", "k_group_norm", "k_group_adamw")
 KERNEL_SRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc", "kernels.hip")
 
 
