@@ -114,8 +114,10 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
   const void* g = P.chunk_grads[q];
   double norm;
   bool finite;
-  if (SPLIT && P.n_partials > 0) {
-    const double t = block_sum(int(threadIdx.x) < P.n_partials ? P.partials[threadIdx.x] : 0.0);
+  if (P.n_partials > 0) {
+    double s = 0.0;
+    for (int i = int(threadIdx.x); i < P.n_partials; i += kBlock) s += P.partials[i];
+    const double t = block_sum(s);
     norm = sqrt(t);
     finite = __builtin_isfinite(t);
   } else {
@@ -137,7 +139,6 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
 
 template <typename In, bool CODED>
 void group_step(const GroupStepLaunch& a, hipStream_t s) {
-  static_assert(kFoldChunks <= kSplitChunks && kFoldChunks <= kBlock, "one partial per lane, split launches");
   const int64_t n = a.q_end - a.q_begin;
   if (n <= kSplitChunks)
     hipLaunchKernelGGL((k_group_adamw<In, CODED, true>), dim3(unsigned(4 * n)), dim3(kBlock), 0, s, a);

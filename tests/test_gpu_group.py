@@ -141,7 +141,8 @@ def run(case, grads, n, max_norm, step):
     case.group.norm(grads, n)
     norm, sq, finite = case.group.get_norm()
     want = oracle_norm(grads, n)
-    # squares are exact in FP64 and each of at most 12 + log2(elements) additions on a value's way rounds once
+    # squares are exact in FP64; on a value's way to the total lie at most 64 additions in its lane, 6 in the wave, 8 in
+    # a lane of the second stage and 6 + 3 twice behind it: under 100 roundings of 2^-53, half as much on the root
     assert finite and abs(norm - want) <= 64 * 2.0 ** -53 * want, (norm, want)
     assert sq == pytest.approx(norm * norm, rel=1e-14)
     case.group.clip_adamw(max_norm, HP, step)
@@ -207,17 +208,20 @@ def test_many_tensors(count):
     assert case.arena.guards_untouched()
 
 
-@pytest.mark.parametrize("chunks", [127, 128, 129, 512, 513])
+@pytest.mark.parametrize("chunks", [127, 128, 129, 512, 2048, 2049])
 def test_sizes_around_the_launch_rules(chunks):
     """Numbers of chunks where the launches change (a step split four ways, the
     norm's second stage left to the step), of one kind and of two."""
-    for parts in ([chunks * 4096 - 5], [(chunks - 1) * 4096, 1], [4096] * 3 + [(chunks - 4) * 4096 - 9, 70]):
+    layouts = [[chunks * 4096 - 5], [(chunks - 1) * 4096, 1], [4096] * 3 + [(chunks - 4) * 4096 - 9, 70]]
+    for parts in layouts[:3 if chunks < 600 else 2]:
         case = Case(parts, [8 if i % 2 == 0 else 32 for i in range(len(parts))], [BF16] * len(parts), seed=chunks)
         assert case.group.info["n_chunks"] == chunks
         before = case.state()
         grads = case.gradients()
         case.group.norm(grads, 1)
         norm = case.group.get_norm()[0]
+        want = math.sqrt(sum(float(np.sum(M.as_f32(host(g)).astype(np.float64) ** 2)) for g in grads))
+        assert abs(norm - want) <= 128 * 2.0 ** -53 * want     # the order of numpy's sum is another one
         case.group.clip_adamw(0.5, HP, 2)
         torch.cuda.synchronize()
         check_step(case, before, grads, 1, 0.5, 2, norm, exact=False)
