@@ -103,10 +103,10 @@ class DeviceState:
         8 bits, decoded ones (zeros between buckets), on the current stream
         after the work that the state's stream has been given."""
         import torch
-        if self.coded is None:
-            return self.m, self.v
         here = torch.cuda.current_stream(self.device)
         here.wait_stream(self.stream)
+        if self.coded is None:
+            return self.m, self.v
         m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
         B.gro_moments_decode(self.plan.handle, self.coded, m.data_ptr(), v.data_ptr(), here.cuda_stream)
         return m, v
@@ -119,14 +119,14 @@ class DeviceState:
             if t.dtype != torch.float32 or t.shape != self.master.shape:
                 raise ValueError(f"{name}: flat FP32 moments have shape {tuple(self.master.shape)}, "
                                  f"got {t.dtype} {tuple(t.shape)}")
+        here = torch.cuda.current_stream(self.device)
+        here.wait_stream(self.stream)
         if self.coded is None:
             self.m.copy_(m)
             self.v.copy_(v)
-            return
-        here = torch.cuda.current_stream(self.device)
-        here.wait_stream(self.stream)
-        m, v = m.to(self.device).contiguous(), v.to(self.device).contiguous()
-        B.gro_moments_encode(self.plan.handle, m.data_ptr(), v.data_ptr(), self.coded, here.cuda_stream)
+        else:
+            m, v = m.to(self.device).contiguous(), v.to(self.device).contiguous()
+            B.gro_moments_encode(self.plan.handle, m.data_ptr(), v.data_ptr(), self.coded, here.cuda_stream)
         self.stream.wait_stream(here)
 
     def grad_buffers(self) -> List:
@@ -246,12 +246,8 @@ class TensorGroup:
     def norm(self, grads: Sequence, window_size: int = 1, stream=None) -> None:
         """gro_group_norm of ``grads`` (one per tensor, None for a tensor left
         out of this step) on ``stream``, by default the current one."""
-        import torch
         ptrs = self._pointers(grads)
-        if stream is not None and stream != torch.cuda.current_stream(self.device.index):
-            for g in grads:  # their memory is not handed out again before that stream is done with it
-                if g is not None:
-                    g.record_stream(stream)
+        self._record(grads, stream)
         with self._here():
             B.gro_group_norm(self.handle, ptrs, window_size, self._stream(stream))
         self._grads = list(grads)  # in place until clip_adamw has been enqueued
@@ -284,8 +280,19 @@ class TensorGroup:
             return contextlib.nullcontext()
         return torch.cuda.device(self.device)
 
+    def _record(self, grads, stream) -> None:
+        """Gradients used on a stream that is not the current one: their memory
+        is not handed out again before that stream is done with it."""
+        import torch
+        if stream is not None and grads is not None and stream != torch.cuda.current_stream(self.device.index):
+            for g in grads:
+                if g is not None:
+                    g.record_stream(stream)
+
     def clip_adamw(self, max_norm: float, hp: dict, step: int, stream=None) -> None:
-        """gro_group_clip_adamw of the gradients given to ``norm``."""
+        """gro_group_clip_adamw of the gradients given to ``norm``, on
+        ``stream``, by default the current one."""
+        self._record(self._grads, stream)
         with self._here():
             B.gro_group_clip_adamw(self.handle, max_norm, hp, step, self._stream(stream))
         self._grads = None

@@ -154,9 +154,10 @@ def save_device_state(st, step: int, directory: str) -> None:
 def load_device_state(st, directory: str) -> int:
     """load_state into a buffers.DeviceState, with moments of 32 or 8 bits;
     returns the step."""
-    if st.coded is None:
-        return load_state(st.plan, st.master, st.m, st.v, directory)
+    import torch
     m, v = st.moments()
     step = load_state(st.plan, st.master, m, v, directory)
-    st.set_moments(m, v)
+    if st.coded is not None:
+        st.set_moments(m, v)
+    st.stream.wait_stream(torch.cuda.current_stream(st.device))
     return step

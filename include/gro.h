@@ -351,13 +351,13 @@ int gro_init_uniform(gro_plan* plan, uint64_t seed, const double* bounds, const 
  *      nothing above it occurs.  Value: (code * s)^2.  A v > 0 never gets the
  *      code 0.
  * Nearest means ties to even; the quotients are FP32, so a value within 2^-22
- * of the border between two codes may get either.  A block's largest element is held exactly, and
- * encoding what was decoded gives the same codes and scales (unless a value
- * leaves FP32's normal range on the way).  m comes back within 2^-4 of itself
- * or 2^-18 of its block's largest; sqrt(v) within 2^-5 of itself or 2^-18 of
- * its block's largest.  An infinite v is held as the largest finite one; a
- * NaN or negative v, or a NaN or infinite m, makes that moment NaN in its
- * whole block.
+ * of the border between two codes may get either.  A block's largest element
+ * is held exactly, and encoding what was decoded gives the same codes and
+ * scales (unless a value leaves FP32's normal range on the way).  m comes back
+ * within 2^-4 of itself or 2^-18 of its block's largest; sqrt(v) within 2^-5 of
+ * itself or 2^-18 of its block's largest.  An infinite v is held as the largest
+ * finite one; a NaN or negative v, or a NaN or infinite m, makes that moment
+ * NaN in its whole block.
  * In a plan a block is [64 k, 64 k + 64) of the flat arrays -- bucket bases
  * are multiples of 64, so no block spans two buckets; the part of a block past
  * the end of its bucket does not enter the scale and its bytes stay as they

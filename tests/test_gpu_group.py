@@ -99,10 +99,10 @@ def oracle_norm(grads, n):
                                for x in M.window_gradient(M.as_f32(host(g)), n)))
 
 
-def check_step(case, before, grads, n, max_norm, step, norm, exact=True):
+def check_step(case, before, grads, n, max_norm, step, norm, exact=True, hp=HP):
     coef, taken = M.clip_coefficient(norm, max_norm)
     assert taken
-    sc = M.adamw_scalars(*[HP[k] for k in ("lr", "beta1", "beta2", "eps", "weight_decay")], step)
+    sc = M.adamw_scalars(*[hp[k] for k in ("lr", "beta1", "beta2", "eps", "weight_decay")], step)
     after = case.state()
     for i, (got, was, g) in enumerate(zip(after, before, grads)):
         if g is None:
@@ -180,6 +180,25 @@ def test_mixed_kinds_and_tensors_without_a_gradient():
     run(case, case.gradients(), 1, 1.0, 3)                    # back again
     run(case, [None] * len(sizes), 1, 1.0, 4)                 # a norm of 0, nothing changes
     assert case.arena.guards_untouched()
+
+
+EXTREMES = [dict(beta1=0.0, beta2=0.0), dict(beta2=0.0, eps=0.0), dict(beta1=0.999999, beta2=1 - 2.0 ** -40),
+            dict(lr=0.0), dict(lr=100.0, weight_decay=10.0), dict(eps=1e30), dict(weight_decay=0.0, eps=1e-30)]
+
+
+@pytest.mark.parametrize("extreme", EXTREMES, ids=[",".join(e) for e in EXTREMES])
+def test_extreme_hyper_parameters(extreme):
+    hp = dict(HP, **extreme)
+    case = Case([4096, 5000, 63], [32, 8, 8], [BF16, BF16, FP32], seed=6)
+    for step, max_norm, n, sigma in ((1, float("inf"), 7, 1.0), (10 ** 9, -1.0, 1, 1e-18), (2, 1e-30, 2, 1e15)):
+        before = case.state()
+        grads = case.gradients(sigma=sigma)
+        case.group.norm(grads, n)
+        norm = case.group.get_norm()[0]
+        case.group.clip_adamw(max_norm, hp, step)
+        torch.cuda.synchronize()
+        with np.errstate(all="ignore"):
+            check_step(case, before, grads, n, max_norm, step, norm, exact=False, hp=hp)
 
 
 def test_one_gradient_for_two_tensors():
