@@ -248,7 +248,7 @@ def _pointer_array(ptrs: Sequence[int], expected: int, what: str):
     reading any); a list of another length must never reach it."""
     if expected and len(ptrs) != expected:
         raise ValueError(f"{what}: {len(ptrs)} pointers given, the call reads {expected}")
-    return (ctypes.c_void_p * max(len(ptrs), 1))(*[ctypes.c_void_p(int(p)) for p in ptrs])
+    return (ctypes.c_void_p * max(len(ptrs), 1))(*map(int, ptrs))
 
 
 # A window or group call takes at most this many microbatches (include/gro.h).
@@ -259,7 +259,9 @@ def _reads(plan: int, b0: int, b1: int, n: int = 1) -> int:
     """Pointers the library reads for buckets [b0, b1) and n microbatches:
     n * (b1 - b0) for a valid range and group size, else 0 (the library then
     rejects the call, or does nothing, before reading a pointer)."""
-    nb = gro_plan_get_info(plan)["n_buckets"]
+    info = gro_plan_info()
+    _check(load().gro_plan_get_info(plan, ctypes.byref(info)))
+    nb = info.n_buckets
     if not (0 <= int(b0) < int(b1) <= nb and 1 <= int(n) <= GRO_MAX_GROUP):
         return 0
     return int(n) * (int(b1) - int(b0))
