@@ -101,7 +101,8 @@ class DeviceState:
     def moments(self):
         """The moments as flat FP32 arrays (m, v): the state's own, or, held in
         8 bits, decoded ones (zeros between buckets), on the current stream
-        after the work that the state's stream has been given."""
+        after the work that the state's stream has been given.  The state's
+        stream waits for the decoding, whose codes its next step writes."""
         import torch
         here = torch.cuda.current_stream(self.device)
         here.wait_stream(self.stream)
@@ -109,6 +110,7 @@ class DeviceState:
             return self.m, self.v
         m, v = torch.zeros_like(self.master), torch.zeros_like(self.master)
         B.gro_moments_decode(self.plan.handle, self.coded, m.data_ptr(), v.data_ptr(), here.cuda_stream)
+        self.stream.wait_stream(here)
         return m, v
 
     def set_moments(self, m, v) -> None:

@@ -398,6 +398,31 @@ def test_a_state_on_a_stream_of_its_own():
         same_bits(got, want, "stream")
 
 
+def test_moments_between_steps_on_a_stream_of_its_own():
+    """Moments read from the current stream after every step, the next step
+    given to the state's stream at once: each reading is of one step."""
+    tensors = specs([3_000_000, 4096])
+    stream = torch.cuda.Stream()
+    plan = Plan(tensors, 2, 1 << 22)
+    st = DeviceState(plan, "cuda", stream=stream, coded_moments=True)
+    ref = DeviceState(Plan(tensors, 2, 1 << 22), "cuda", coded_moments=True)
+    grads = [torch.randn(b.shape, device="cuda").to(b.dtype) for b in st.grad_buffers()]
+    torch.cuda.synchronize()
+    found = []
+    for state, s in ((st, stream), (ref, torch.cuda.current_stream())):
+        h, nb, acc = state.plan.handle, plan.info["n_buckets"], state.acc.data_ptr()
+        read = []
+        for step in range(1, 6):
+            B.gro_accumulate_window(h, 0, nb, [g.data_ptr() for g in grads], 1, acc, s.cuda_stream)
+            B.gro_reduce_norm(h, acc, 1, s.cuda_stream)
+            B.gro_clip_adamw_coded(h, acc, 1, 1.0, HP, step, state.master.data_ptr(), state.coded,
+                                   state.p_bf16.data_ptr(), s.cuda_stream)
+            read += state.moments()
+        found.append([host(x) for x in read])
+    for got, want in zip(*found):
+        same_bits(got, want, "moments")
+
+
 def test_checkpoints_carry_8_bit_moments(tmp_path):
     """Saved after two steps and restored into a fresh state of the same
     layout, the third step is the uninterrupted run's bit for bit; restored
