@@ -87,7 +87,8 @@ class DeviceState:
         if not static_workspace:
             nbytes = int(plan.info["workspace_bytes"])
             self.workspace = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
-        # the zeros above are written on the current stream
+        # the arrays' memory and zeros are the current stream's
+        self._keep(x for x in vars(self).values() if isinstance(x, torch.Tensor))
         self.stream.wait_stream(torch.cuda.current_stream(self.device))
         if static_workspace:
             self.workspace, self.ws_ptr, self.ws_bytes = None, None, 0
@@ -97,6 +98,14 @@ class DeviceState:
         self.ws_ptr = (base + 255) // 256 * 256
         self.ws_bytes = nbytes
         B.gro_plan_bind(plan.handle, self.ws_ptr, nbytes, self.stream.cuda_stream)
+
+    def _keep(self, tensors) -> None:
+        """Tensors of the current stream that the state's stream uses: their
+        memory is not handed out again before that stream is done with it."""
+        import torch
+        if self.stream != torch.cuda.current_stream(self.device):
+            for t in tensors:
+                t.record_stream(self.stream)
 
     def moments(self):
         """The moments as flat FP32 arrays (m, v): the state's own, or, held in
@@ -132,13 +141,15 @@ class DeviceState:
         self.stream.wait_stream(here)
 
     def grad_buffers(self) -> List:
-        """One [slots, slot_stride] buffer per bucket (zeros), BF16 or FP32
-        as the bucket's gradient type says."""
+        """One [slots, slot_stride] buffer per bucket (zeros, written on the
+        current stream), BF16 or FP32 as the bucket's gradient type says."""
         import torch
-        return [torch.zeros((bk["slots"], bk["slot_stride"]),
+        bufs = [torch.zeros((bk["slots"], bk["slot_stride"]),
                             dtype=torch.float32 if bk["grad_dtype"] == B.GRO_GRAD_FP32 else torch.bfloat16,
                             device=self.device)
                 for bk in self.plan.buckets]
+        self._keep(bufs)
+        return bufs
 
     def pack(self, bufs: List, i: int, slot_grads: Sequence) -> None:
         """Copy tensor i's per-slot gradients (1-D, length numel, the

@@ -423,6 +423,41 @@ def test_moments_between_steps_on_a_stream_of_its_own():
         same_bits(got, want, "moments")
 
 
+def test_a_state_dropped_with_steps_still_on_its_stream():
+    """Codes, scales, accumulator, workspace and gradient buffers of a dropped
+    state stay as they are until the steps on its stream are done, whatever is
+    allocated and written on the current stream meanwhile."""
+    tensors = specs([3_000_000, 4096])
+    stream = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    found = []
+    for s in (stream, torch.cuda.current_stream()):
+        plan = Plan(tensors, 2, 1 << 22)
+        st = DeviceState(plan, "cuda", stream=s, coded_moments=True)
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        grads = st.grad_buffers()
+        for g in grads:
+            g.copy_(torch.randn(g.shape, generator=gen, device="cuda"))
+        master, sizes = st.master, [x.numel() for x in (st.acc, st.m_code, st.m_scale, st.workspace, *grads)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):                 # some milliseconds in front of the steps
+                busy @ busy
+        h, nb, acc = plan.handle, plan.info["n_buckets"], st.acc.data_ptr()
+        for step in (1, 2, 3):
+            B.gro_accumulate_window(h, 0, nb, [g.data_ptr() for g in grads], 1, acc, s.cuda_stream)
+            B.gro_reduce_norm(h, acc, 1, s.cuda_stream)
+            B.gro_clip_adamw_coded(h, acc, 1, 1.0, HP, step, master.data_ptr(), st.coded, st.p_bf16.data_ptr(),
+                                   s.cuda_stream)
+        del st, grads, g
+        junk = [torch.full((n * size,), POISON, dtype=torch.uint8, device="cuda") for n in sizes for size in (1, 2, 4)]
+        torch.cuda.synchronize()
+        found.append(host(master))
+        del junk
+    same_bits(found[0], found[1], "master")
+    assert found[0].any()
+
+
 def test_checkpoints_carry_8_bit_moments(tmp_path):
     """Saved after two steps and restored into a fresh state of the same
     layout, the third step is the uninterrupted run's bit for bit; restored

@@ -13,7 +13,7 @@ class Stream:
     stream has been given so far."""
 
     def __init__(self, handle):
-        self.cuda_stream, self.done = handle, []
+        self.cuda_stream, self.done, self.kept = handle, [], []
 
     def wait_stream(self, other):
         self.done += [x for x in other.done if x not in self.done]
@@ -33,6 +33,8 @@ def streams(monkeypatch):
 
     for name in ("gro_plan_bind", "gro_moments_decode", "gro_moments_encode"):
         monkeypatch.setattr(B, name, note(name))
+    # what the allocator is told of a tensor used on a stream other than the one it was allocated on
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: s.kept.append(t.data_ptr()))
     return here, side
 
 
@@ -60,3 +62,20 @@ def test_a_step_after_set_moments_waits_for_the_encoding(streams):
     st.set_moments(zeros, zeros)
     assert here.done.index("step") < here.done.index("gro_moments_encode")
     assert "gro_moments_encode" in side.done
+
+
+@pytest.mark.parametrize("coded", [False, True])
+def test_a_states_memory_outlives_the_work_on_its_stream(streams, coded):
+    """Arrays, workspace and gradient buffers are allocated on the current
+    stream: dropped with steps still running on the state's stream, they must
+    not be handed out again before those are done."""
+    here, side = streams
+    st = DeviceState(plan(), "cpu", stream=side, coded_moments=coded)
+    arrays = [x for x in vars(st).values() if isinstance(x, torch.Tensor)]
+    assert len(arrays) == (8 if coded else 6)
+    bufs = st.grad_buffers()
+    assert {x.data_ptr() for x in arrays + bufs} <= set(side.kept)
+    assert not here.kept
+    own = DeviceState(plan(), "cpu", coded_moments=coded)      # on the current stream: nothing to record
+    own.grad_buffers()
+    assert not here.kept
