@@ -181,7 +181,12 @@ class TensorGroup:
     ``params_bf16``: BF16 copies to update along, None for a tensor without.
     ``states``: per tensor (m, v) or, in 8 bits, (m, v, m_scale, v_scale);
     zeros are allocated when it is not given.  The tensors stay the caller's;
-    the group keeps references to them."""
+    the group keeps references to them.
+
+    A call runs on ``stream``, by default the current one; ordering it after
+    the work that made its inputs is the caller's, as with any operation on
+    another stream.  Memory is not: whatever the group or the caller lets go of
+    stays as it is until the enqueued work is done with it."""
 
     def __init__(self, masters: Sequence, state_bits=32, no_decay=False, grad_dtype=None,
                  params_bf16: Optional[Sequence] = None, states: Optional[Sequence] = None):
@@ -237,13 +242,10 @@ class TensorGroup:
         self._on = [self.device.index] * n
         with self._here():
             # waits for the current stream, and so for the zeros above too
-            B.gro_group_bind(self.handle, rows, (self.workspace.data_ptr() + 255) // 256 * 256, nbytes,
-                             self._stream(None))
-        self._grads = None
-
-    def _stream(self, stream) -> int:
-        import torch
-        return (torch.cuda.current_stream(self.device.index) if stream is None else stream).cuda_stream
+            born = torch.cuda.current_stream(self.device.index).cuda_stream
+            B.gro_group_bind(self.handle, rows, (self.workspace.data_ptr() + 255) // 256 * 256, nbytes, born)
+        self._seen = {born}       # streams that need no (further) recording of the group's own memory
+        self._grads, self._grads_on = None, None
 
     def close(self) -> None:
         if self.handle:
@@ -260,10 +262,10 @@ class TensorGroup:
         """gro_group_norm of ``grads`` (one per tensor, None for a tensor left
         out of this step) on ``stream``, by default the current one."""
         ptrs = self._pointers(grads)
-        self._record(grads, stream)
+        s = self._use(stream, grads)
         with self._here():
-            B.gro_group_norm(self.handle, ptrs, window_size, self._stream(stream))
-        self._grads = list(grads)  # in place until clip_adamw has been enqueued
+            B.gro_group_norm(self.handle, ptrs, window_size, s)
+        self._grads, self._grads_on = list(grads), s  # in place until clip_adamw has been enqueued
 
     def _pointers(self, grads: Sequence) -> List[int]:
         """The gradients' pointers, 0 for None, after checking each: property
@@ -293,22 +295,36 @@ class TensorGroup:
             return contextlib.nullcontext()
         return torch.cuda.device(self.device)
 
-    def _record(self, grads, stream) -> None:
-        """Gradients used on a stream that is not the current one: their memory
-        is not handed out again before that stream is done with it."""
+    def _use(self, stream, grads, recorded=None) -> int:
+        """The handle of the stream that a call runs on.  Memory that the call
+        uses there is recorded with the allocator, so that it is not handed
+        out again before that stream is done with it: the group's own once per
+        stream, gradients in every call, unless they are ``recorded`` on that
+        stream already or both it and the current one are the default stream
+        (0), where gradients usually come from and recording 4000 of them would
+        take longer than the checks."""
         import torch
-        if stream is not None and grads is not None and stream != torch.cuda.current_stream(self.device.index):
+        here = torch.cuda.current_stream(self.device.index)
+        s = here if stream is None else stream
+        handle = s.cuda_stream
+        if handle not in self._seen:
+            for t in (self.workspace, *self.masters, *self.copies, *(x for st in self.states for x in st)):
+                if t is not None:
+                    t.record_stream(s)
+            self._seen.add(handle)
+        if grads is not None and handle != recorded and (handle or here.cuda_stream):
             for g in grads:
                 if g is not None:
-                    g.record_stream(stream)
+                    g.record_stream(s)
+        return handle
 
     def clip_adamw(self, max_norm: float, hp: dict, step: int, stream=None) -> None:
         """gro_group_clip_adamw of the gradients given to ``norm``, on
         ``stream``, by default the current one."""
-        self._record(self._grads, stream)
+        s = self._use(stream, self._grads, self._grads_on)
         with self._here():
-            B.gro_group_clip_adamw(self.handle, max_norm, hp, step, self._stream(stream))
-        self._grads = None
+            B.gro_group_clip_adamw(self.handle, max_norm, hp, step, s)
+        self._grads, self._grads_on = None, None
 
     def get_norm(self):
         """(norm, norm_sq, finite) of the last ``norm``; waits for its stream."""

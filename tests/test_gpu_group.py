@@ -446,6 +446,45 @@ def test_groups_on_streams_and_threads_of_their_own():
                     same_bits(x, y, "streams")
 
 
+@pytest.mark.parametrize("given", [True, False], ids=["stream given", "stream current"])
+def test_a_group_dropped_with_steps_still_on_another_stream(given):
+    """The workspace, the states that the group allocated and the gradients of
+    a dropped group stay as they are until its steps are done, whatever is
+    allocated and written on the default stream meanwhile."""
+    sizes, bits = [3_000_000, 4097, 300], [8, 32, 8]
+    stream = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device="cuda")
+    found = []
+    for s in (stream, torch.cuda.current_stream()):
+        gen = torch.Generator(device="cuda").manual_seed(8)
+        masters = [torch.randn(n, generator=gen, device="cuda") for n in sizes]
+        group = TensorGroup(masters, state_bits=bits)
+        used = [group.workspace.numel(), *(x.numel() * x.element_size() for st in group.states for x in st)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):                 # some milliseconds in front of the steps
+                busy @ busy
+        for step in (1, 2, 3):
+            grads = [torch.randn(n, generator=gen, device="cuda").to(BF16) for n in sizes]
+            ready = torch.cuda.Event()
+            ready.record()
+            s.wait_event(ready)
+            if given:
+                group.norm(grads, 1, s)
+                group.clip_adamw(1.0, HP, step, s)
+            else:
+                with torch.cuda.stream(s):
+                    group.norm(grads)
+                    group.clip_adamw(1.0, HP, step)
+        del group, grads
+        junk = [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for n in used + [2 * n for n in sizes]]
+        torch.cuda.synchronize()
+        found.append([host(p) for p in masters])
+        del junk
+    for got, want in zip(*found):
+        same_bits(got, want, "master")
+
+
 def test_bound_again_to_moved_states():
     case = Case([500, 90], [8, 32], [BF16, BF16])
     run(case, case.gradients(), 1, 1.0, 1)
