@@ -152,12 +152,16 @@ def save_device_state(st, step: int, directory: str) -> None:
 
 
 def load_device_state(st, directory: str) -> int:
-    """load_state into a buffers.DeviceState, with moments of 32 or 8 bits;
-    returns the step."""
+    """load_state into a buffers.DeviceState, with moments of 32 or 8 bits, its
+    BF16 copy the restored master rounded to nearest even; returns the step."""
     import torch
     m, v = st.moments()
     step = load_state(st.plan, st.master, m, v, directory)
     if st.coded is not None:
         st.set_moments(m, v)
+    if st.p_bf16 is not None:
+        for row in st.plan.tensors:
+            if row["updated"] and row["numel"]:
+                _slice(st.p_bf16, row).copy_(_slice(st.master, row))
     st.stream.wait_stream(torch.cuda.current_stream(st.device))
     return step

@@ -7,9 +7,10 @@ import numpy as np
 import pytest
 import torch
 
+from gradient_reduction_optimizer_amd import binding as B
 from gradient_reduction_optimizer_amd import synth
-from gradient_reduction_optimizer_amd.buffers import Plan
-from gradient_reduction_optimizer_amd.checkpoint import CheckpointError, load_state, save_state
+from gradient_reduction_optimizer_amd.buffers import DeviceState, Plan
+from gradient_reduction_optimizer_amd.checkpoint import CheckpointError, load_device_state, load_state, save_state
 
 
 def _states(plan, seed):
@@ -131,3 +132,40 @@ def test_shard_state_restores_only_into_the_same_shard(tmp_path):
     with pytest.raises(CheckpointError):
         load_state(b, *_states(b, 10), directory=str(tmp_path))
     assert load_state(a, *_states(a, 11), directory=str(tmp_path)) == 4
+
+
+@pytest.mark.parametrize("with_bf16", [True, False])
+def test_a_restored_device_state_has_its_bf16_copy(tmp_path, monkeypatch, with_bf16):
+    """The copy is what the next forward pass reads: after a restore it is the
+    restored master rounded to BF16, and what lies between the buckets is left
+    alone.  (The state's arrays on the host, its stream a stand-in.)"""
+    class Stream:
+        cuda_stream = 0
+
+        def wait_stream(self, other):
+            pass
+
+    stream = Stream()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    monkeypatch.setattr(B, "gro_plan_bind", lambda *a: None)
+    w = synth.tiny()
+    a = Plan(w.tensors, w.R, w.bucket_elems)
+    sa = _states(a, 12)
+    save_state(a, *sa, step=5, directory=str(tmp_path))
+    b = Plan(list(reversed(w.tensors)), w.R, 1000)
+    st = DeviceState(b, "cpu", with_bf16=with_bf16)
+    for x in (st.master, st.m, st.v, *([st.p_bf16] if with_bf16 else [])):
+        x.fill_(7.0)
+    assert load_device_state(st, str(tmp_path)) == 5
+    want = _by_pid(a, sa)
+    gap = torch.ones(st.master.numel(), dtype=torch.bool)
+    for i, row in enumerate(b.tensors):
+        if not row["updated"] or not row["numel"]:
+            continue
+        gap[row["flat_offset"]:row["flat_offset"] + row["numel"]] = False
+        for x, y in zip((st.master, st.m, st.v), want[row["param_id"]]):
+            assert torch.equal(st.flat_view(x, i), y)
+        if with_bf16:
+            assert torch.equal(st.flat_view(st.p_bf16, i), want[row["param_id"]][0].to(torch.bfloat16))
+    assert gap.any() and (st.master[gap] == 7.0).all()
+    assert not with_bf16 or (st.p_bf16[gap] == 7.0).all()

@@ -500,6 +500,27 @@ def test_checkpoints_carry_8_bit_moments(tmp_path):
             same_bits(got, want, k)
 
 
+@pytest.mark.parametrize("coded", [True, False])
+def test_a_restored_state_has_its_bf16_copy(tmp_path, coded):
+    """Loaded into a fresh state: the copy is the saved run's bit for bit at
+    once, before any step, and the gaps between the buckets stay."""
+    tensors = specs([30_001, 7, 4096, 10_000])
+    a = Side(tensors, 2, 1 << 20, seed=2)
+    a.window(a.gradients(1))
+    a.update(1, 1.0, 1)
+    C.save_device_state(a.st, 1, str(tmp_path))
+    if coded:
+        b = Side(tensors, 2, 1 << 20, seed=3)
+        st = b.st
+    else:
+        b, st = None, DeviceState(Plan(tensors, 2, 1 << 20), "cuda")
+    assert C.load_device_state(st, str(tmp_path)) == 1
+    torch.cuda.synchronize()
+    for k in range(a.nb):
+        same_bits(host(st.p_bf16[a.span(k)]), host(a.st.p_bf16[a.span(k)]), k)
+    assert b is None or b.gaps_untouched()
+
+
 def test_offsets_past_32_bits():
     """One bucket of more than 2^31 elements: both ends against the oracle."""
     n = 2 ** 31 + 4096 + 77
