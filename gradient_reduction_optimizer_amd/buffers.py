@@ -165,9 +165,12 @@ class DeviceState:
         return arr[off:off + t["numel"]] if off >= 0 else arr[:0]
 
 
-def _check_array(what: str, t, dtype, numel: int, device) -> None:
-    if t.dtype != dtype or t.numel() != numel or t.get_device() != device.index or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous {dtype} tensor of {numel} elements on {device} is needed, got "
+def _check_array(what: str, t, dtype, shape, device) -> None:
+    """A contiguous tensor of this type and shape on this GPU.  A flat one of as
+    many elements has them in the same order, and so does any for a flat shape."""
+    if (t.dtype != dtype or t.numel() != shape.numel() or t.get_device() != device.index or not t.is_contiguous()
+            or (t.shape != shape and t.dim() != 1 and len(shape) != 1)):
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
@@ -175,7 +178,8 @@ class TensorGroup:
     """Many FP32 master tensors stepped at once where they lie, bound to a
     workspace of its own: gro_group_norm and gro_group_clip_adamw.
 
-    ``masters``: contiguous FP32 tensors of one GPU.  Per tensor, as one value
+    ``masters``: contiguous FP32 tensors of one GPU.  A tensor's copy, moments
+    and gradients have its shape, or they or it are flat.  Per tensor, as one value
     for all or a list: ``state_bits`` (32 or 8: how the moments are held),
     ``no_decay``, ``grad_dtype`` (torch.bfloat16 or torch.float32).
     ``params_bf16``: BF16 copies to update along, None for a tensor without.
@@ -215,19 +219,19 @@ class TensorGroup:
         kinds = {32: (torch.float32,) * 2, 8: (torch.uint8,) * 2 + (torch.float32,) * 2}
         for i, p in enumerate(masters):
             k = p.numel()
-            _check_array(f"master {i}", p, torch.float32, k, self.device)
+            _check_array(f"master {i}", p, torch.float32, p.shape, self.device)
             if copies[i] is not None:
-                _check_array(f"params_bf16 {i}", copies[i], torch.bfloat16, k, self.device)
+                _check_array(f"params_bf16 {i}", copies[i], torch.bfloat16, p.shape, self.device)
             dtypes = kinds[bits[i]]
-            blocks = -(-k // B.GRO_CODED_BLOCK)
-            sizes = (k, k, blocks, blocks)[:len(dtypes)]
+            blocks = torch.Size([-(-k // B.GRO_CODED_BLOCK)])
+            shapes = (p.shape, p.shape, blocks, blocks)[:len(dtypes)]
             if states is None:
-                st = tuple(torch.zeros(s, dtype=d, device=self.device) for s, d in zip(sizes, dtypes))
+                st = tuple(torch.zeros(s.numel(), dtype=d, device=self.device) for s, d in zip(shapes, dtypes))
             else:
                 st = tuple(states[i])
                 if len(st) != len(dtypes):
                     raise ValueError(f"states {i}: {len(dtypes)} tensors are needed, got {len(st)}")
-                for t, s, d in zip(st, sizes, dtypes):
+                for t, s, d in zip(st, shapes, dtypes):
                     _check_array(f"states {i}", t, d, s, self.device)
             self.states.append(st)
             rows.append([p.data_ptr(), *[t.data_ptr() for t in st], *[0] * (4 - len(st)),
@@ -238,7 +242,7 @@ class TensorGroup:
         self.info = B.gro_group_get_info(self.handle)
         nbytes = int(self.info["workspace_bytes"])
         self.workspace = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
-        self._numels = [p.numel() for p in masters]
+        self._shapes = [p.shape for p in masters]
         self._on = [self.device.index] * n
         with self._here():
             # waits for the current stream, and so for the zeros above too
@@ -276,7 +280,7 @@ class TensorGroup:
             raise ValueError(f"{len(grads)} gradients for {len(self.masters)} tensors")
         T = torch.Tensor
         try:
-            if (list(map(T.numel, grads)) == self._numels and list(map(T.get_device, grads)) == self._on
+            if (list(map(T.size, grads)) == self._shapes and list(map(T.get_device, grads)) == self._on
                     and list(map(attrgetter("dtype"), grads)) == self.grad_dtype and all(map(T.is_contiguous, grads))):
                 return list(map(T.data_ptr, grads))
         except TypeError:  # None among them
@@ -284,7 +288,7 @@ class TensorGroup:
         ptrs = []
         for i, g in enumerate(grads):
             if g is not None:
-                _check_array(f"gradient {i}", g, self.grad_dtype[i], self._numels[i], self.device)
+                _check_array(f"gradient {i}", g, self.grad_dtype[i], self._shapes[i], self.device)
             ptrs.append(0 if g is None else g.data_ptr())
         return ptrs
 
