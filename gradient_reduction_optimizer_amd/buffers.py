@@ -250,6 +250,7 @@ class TensorGroup:
             B.gro_group_bind(self.handle, rows, (self.workspace.data_ptr() + 255) // 256 * 256, nbytes, born)
         self._seen = {born}       # streams that need no (further) recording of the group's own memory
         self._grads, self._grads_on = None, None
+        self._written = self._all = [*self.masters, *(c for c in copies if c is not None)]
 
     def close(self) -> None:
         if self.handle:
@@ -270,6 +271,8 @@ class TensorGroup:
         with self._here():
             B.gro_group_norm(self.handle, ptrs, window_size, s)
         self._grads, self._grads_on = list(grads), s  # in place until clip_adamw has been enqueued
+        self._written = self._all if 0 not in ptrs else [t for q, (p, c) in zip(ptrs, zip(self.masters, self.copies))
+                                                         if q for t in (p, c) if t is not None]
 
     def _pointers(self, grads: Sequence) -> List[int]:
         """The gradients' pointers, 0 for None, after checking each: property
@@ -324,11 +327,16 @@ class TensorGroup:
 
     def clip_adamw(self, max_norm: float, hp: dict, step: int, stream=None) -> None:
         """gro_group_clip_adamw of the gradients given to ``norm``, on
-        ``stream``, by default the current one."""
+        ``stream``, by default the current one.  Counts as an operation in
+        place on the masters and copies it writes, so that autograd refuses a
+        backward pass through a graph that saved them from before (a replay of
+        a captured step does not: nothing tells autograd of it)."""
+        import torch
         s = self._use(stream, self._grads, self._grads_on)
         with self._here():
             B.gro_group_clip_adamw(self.handle, max_norm, hp, step, s)
-        self._grads, self._grads_on = None, None
+        torch.autograd.graph.increment_version(self._written)
+        self._grads, self._grads_on, self._written = None, None, self._all
 
     def get_norm(self):
         """(norm, norm_sq, finite) of the last ``norm``; waits for its stream."""

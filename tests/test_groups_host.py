@@ -74,3 +74,43 @@ def test_states_and_copies_of_another_shape_are_refused():
                 dict(states=[(ones(4, 8), ones(2, 16))]), dict(state_bits=8, states=[(codes[0], codes[1].view(8, 4), *scales)])):
         with pytest.raises(ValueError, match=r"\(4, 8\)"):
             TensorGroup([p], **bad)
+
+
+def test_a_step_behind_a_saved_tensors_back_is_seen():
+    """A backward pass through a graph that saved a master or a copy from
+    before the step would use its new values: autograd raises, as it does for
+    torch's own operations in place."""
+    p, w = ones(4, 8).requires_grad_(), ones(4, 8, dtype=BF16).requires_grad_()
+    group = TensorGroup([p, ones(32)], params_bf16=[w, None])
+    for saved in (p, w):
+        loss = (saved * saved).sum()
+        group.norm([ones(4, 8, dtype=BF16), ones(32, dtype=BF16)])
+        group.clip_adamw(1.0, HP, 1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        (saved * saved).sum().backward()        # a new graph is as good as ever
+
+
+def test_only_what_a_step_writes_counts_as_modified():
+    """Left out, refused and failing calls leave versions alone; tensors made
+    in inference mode have none and are stepped all the same."""
+    p, q = ones(4, 8).requires_grad_(), ones(32).requires_grad_()
+    with torch.inference_mode():
+        r = ones(5)
+    group = TensorGroup([p, q, r])
+    grads = [ones(4, 8, dtype=BF16), None, ones(5, dtype=BF16)]
+    versions = [x._version for x in (p, q)]
+    loss = (q * q).sum()
+    group.norm(grads)
+    assert [x._version for x in (p, q)] == versions          # a norm writes none of them
+    group.clip_adamw(1.0, HP, 1)
+    assert p._version > versions[0] and q._version == versions[1]
+    loss.backward()
+    with pytest.MonkeyPatch.context() as m:
+        def fails(*a):
+            raise B.GroError(B.GRO_E_STATE, "refused")
+        m.setattr(B, "gro_group_clip_adamw", fails)
+        version = p._version
+        with pytest.raises(B.GroError):
+            group.clip_adamw(1.0, HP, 2)
+        assert p._version == version
