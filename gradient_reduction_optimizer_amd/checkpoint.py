@@ -59,6 +59,13 @@ def _slice(arr, row):
     return arr[off:off + row["numel"]]
 
 
+def _check_floats(master, m, v) -> None:
+    for name, arr in (("master", master), ("m", m), ("v", v)):
+        if arr is None or not arr.is_floating_point():
+            raise CheckpointError(f"{name}: a flat floating-point array is needed (8-bit moments: save_device_state, "
+                                  "load_device_state)")
+
+
 def save_state(plan, master, m, v, step: int, directory: str) -> None:
     """Write the owned state of every updated parameter of ``plan``.
 
@@ -71,9 +78,7 @@ def save_state(plan, master, m, v, step: int, directory: str) -> None:
     import torch
     from safetensors.torch import save_file
 
-    for name, arr in (("master", master), ("m", m), ("v", v)):
-        if arr is None or arr.dtype != torch.float32:
-            raise CheckpointError(f"{name}: flat FP32 arrays are saved (8-bit moments: save_device_state)")
+    _check_floats(master, m, v)
     os.makedirs(directory, exist_ok=True)
     manifest = os.path.join(directory, MANIFEST)
     if os.path.exists(manifest):
@@ -110,6 +115,7 @@ def load_state(plan, master, m, v, directory: str) -> int:
     """
     from safetensors.torch import load_file
 
+    _check_floats(master, m, v)
     if not os.path.exists(os.path.join(directory, MANIFEST)):
         raise CheckpointError(f"{directory}: no {MANIFEST} manifest, the save did not complete")
     with open(os.path.join(directory, META_FILE)) as f:

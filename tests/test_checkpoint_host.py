@@ -169,3 +169,28 @@ def test_a_restored_device_state_has_its_bf16_copy(tmp_path, monkeypatch, with_b
             assert torch.equal(st.flat_view(st.p_bf16, i), want[row["param_id"]][0].to(torch.bfloat16))
     assert gap.any() and (st.master[gap] == 7.0).all()
     assert not with_bf16 or (st.p_bf16[gap] == 7.0).all()
+
+
+def test_codes_are_refused_on_both_ways_and_other_floats_are_not(tmp_path):
+    """Code bytes of 8-bit moments are no moments: neither saved as such nor
+    overwritten with moments rounded to whole numbers.  States in another
+    floating type pass, as they always have."""
+    w = synth.tiny()
+    a = Plan(w.tensors, w.R, w.bucket_elems)
+    master, m, v = _states(a, 13)
+    save_state(a, master, m, v, step=1, directory=str(tmp_path))
+    for k in range(3):
+        for bad in (torch.zeros(master.numel(), dtype=torch.uint8), None):
+            arrays = [torch.zeros_like(master) for _ in range(3)]
+            arrays[k] = bad
+            with pytest.raises(CheckpointError, match=("master", "m", "v")[k]):
+                load_state(a, *arrays, directory=str(tmp_path))
+            assert not any(x.any() for x in arrays if x is not None)
+            with pytest.raises(CheckpointError, match=("master", "m", "v")[k]):
+                save_state(a, *arrays, step=2, directory=str(tmp_path))
+    wide = [x.double() for x in (master, m, v)]
+    save_state(a, *wide, step=3, directory=str(tmp_path))
+    back = [torch.zeros_like(x) for x in wide]
+    assert load_state(a, *back, directory=str(tmp_path)) == 3
+    got, want = _by_pid(a, back), _by_pid(a, wide)
+    assert all(torch.equal(x, y) for pid in want for x, y in zip(got[pid], want[pid]))
