@@ -1,6 +1,6 @@
 // C-ABI entry points of groups: tensors that stay where they lie.  As for
 // plans, every check happens on the host before the first launch, so a call
-// that returns an error has enqueued nothing.
+// that is refused has enqueued nothing.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
@@ -249,7 +249,10 @@ extern "C" int gro_group_norm(gro_group* g, const void* const* d_grads, int32_t 
       return set_error(GRO_E_INVALID, "gradient of tensor %d is not aligned to its elements", e.given);
 
   hipStream_t s = static_cast<hipStream_t>(stream);
-  g->norm_done = false;  // from here on the pointers of an earlier call are being replaced
+  // From here on the pointers and partials of an earlier call are being
+  // replaced: a launch that fails midway leaves no norm at all.
+  g->norm_done = false;
+  g->norm_valid = false;
   GroupNormArgs a;
   a.chunks = dev_chunks(g);
   a.chunk_grads = dev_grads(g);
@@ -286,13 +289,13 @@ extern "C" int gro_group_clip_adamw(gro_group* g, double max_norm, const gro_ada
   a.partials = dev_partials(g);
   a.n_partials = folded(g) ? int32_t(g->n_chunks) : 0;
   a.k = adamw_consts(*hp, step, max_norm, g->window);
+  g->norm_done = false;  // one update for one norm, also when a launch fails after others have updated their kind
   for (int kind = 0; kind < 4; ++kind) {
     a.q_begin = g->kind_chunk[kind];
     a.q_end = g->kind_chunk[kind + 1];
     const hipError_t e = launch_group_step(a, (kind & 2) != 0, (kind & 1) != 0, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "group clip+AdamW launch");
   }
-  g->norm_done = false;
   return GRO_OK;
 }
 

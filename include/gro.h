@@ -458,7 +458,10 @@ int gro_group_norm(gro_group* group, const void* const* d_grads, int32_t window_
 /* Clip + AdamW of the gradients given to the last gro_group_norm, per element
  * as gro_clip_adamw; a non-finite norm leaves everything bit-unchanged.  Needs a
  * gro_group_norm since the last call (else GRO_E_STATE), on the same stream or
- * ordered before this one. */
+ * ordered before this one.  GRO_E_HIP from one of the call's launches (one per
+ * kind of tensor) may leave other kinds updated; the update is not repeated, the
+ * next one needs a new norm.  After GRO_E_HIP from gro_group_norm there is no
+ * norm, the last one's included. */
 int gro_group_clip_adamw(gro_group* group, double max_norm, const gro_adamw_hparams* hp, int64_t step,
                          void* stream);
 
