@@ -539,7 +539,7 @@ Range flat_range(const gro_plan* p, const void* a, uint64_t elem_bytes) {
 }
 
 // The 8-bit moments' pointers, and that they overlap neither each other nor
-// the call's other (at most four) arrays.
+// the workspace nor the call's other (at most three) arrays.
 int check_coded(const gro_plan* p, const gro_coded_moments* c, std::initializer_list<Range> others) {
   if (c == nullptr) return set_error(GRO_E_INVALID, "moments is NULL");
   if (p->buckets.empty()) return GRO_OK;
@@ -551,6 +551,7 @@ int check_coded(const gro_plan* p, const gro_coded_moments* c, std::initializer_
   Range r[8];
   size_t k = 0;
   for (int i = 0; i < 4; ++i) r[k++] = Range{reinterpret_cast<uintptr_t>(all[i]), i < 2 ? n : scales};
+  r[k++] = Range{reinterpret_cast<uintptr_t>(p->d_ws), p->ws.total};
   for (const Range& o : others) r[k++] = o;
   if (first_overlap(r, k) >= 0) return set_error(GRO_E_INVALID, "arrays of the call overlap");
   return GRO_OK;

@@ -112,10 +112,11 @@ int fill_group(gro_group* g, const gro_group_desc* tensors, int32_t n) {
   return GRO_OK;
 }
 
-// The device chunk table from the caller's pointers.
-int fill_chunks(const gro_group* g, const gro_group_tensor* tensors, std::vector<GroupChunkDev>& out) {
+// The device chunk table from the caller's pointers, for a workspace at ws.
+int fill_chunks(const gro_group* g, const gro_group_tensor* tensors, const char* ws, std::vector<GroupChunkDev>& out) {
   std::vector<Range> written;
-  written.reserve(g->entries.size() * 6);
+  written.reserve(g->entries.size() * 6 + 1);
+  written.push_back(Range{reinterpret_cast<uintptr_t>(ws), g->total});
   int32_t index = 0;
   for (const gro_group::Entry& e : g->entries) {
     const gro_group_tensor& t = tensors[e.given];
@@ -158,14 +159,14 @@ int fill_chunks(const gro_group* g, const gro_group_tensor* tensors, std::vector
     ++index;
   }
   if (first_overlap(written.data(), written.size()) >= 0)
-    return set_error(GRO_E_DUPLICATE, "two of the group's arrays overlap: an element would be updated twice");
+    return set_error(GRO_E_DUPLICATE, "two of the group's arrays, or one and the workspace, overlap");
   return GRO_OK;
 }
 
 int bind_group(gro_group* g, const gro_group_tensor* tensors, char* ws, hipStream_t s) {
   std::vector<GroupChunkDev> chunks;
   chunks.reserve(size_t(g->n_chunks));
-  const int rc = fill_chunks(g, tensors, chunks);
+  const int rc = fill_chunks(g, tensors, ws, chunks);
   if (rc != GRO_OK) return rc;
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);

@@ -366,8 +366,8 @@ int gro_init_uniform(gro_plan* plan, uint64_t seed, const double* bounds, const 
 
 /* Device pointers of a plan's 8-bit moments: n_flat code bytes each and
  * n_flat / GRO_CODED_BLOCK scales each (all zeros = moments of zero).  16-byte
- * aligned; the four arrays, the other arrays of a call and the BF16 copy must
- * not overlap. */
+ * aligned; the four arrays, the other arrays of a call, the BF16 copy and the
+ * workspace must not overlap. */
 typedef struct gro_coded_moments {
   uint8_t* m;
   uint8_t* v;
@@ -441,8 +441,8 @@ int gro_group_get_info(const gro_group* group, gro_group_info* info);
 /* Upload the tables into the caller's workspace (>= workspace_bytes, 256-byte
  * aligned) on `stream` and wait.  tensors: host array of n_tensors entries, read
  * only during the call.  An array that would be written twice -- a tensor given
- * twice, or overlapping views -- is GRO_E_DUPLICATE.  May be repeated, for
- * example when a state has moved. */
+ * twice, overlapping views, or one that overlaps the workspace -- is
+ * GRO_E_DUPLICATE.  May be repeated, for example when a state has moved. */
 int gro_group_bind(gro_group* group, const gro_group_tensor* tensors, void* d_workspace, uint64_t bytes,
                    void* stream);
 

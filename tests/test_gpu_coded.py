@@ -307,6 +307,32 @@ def test_refusals_change_nothing():
         st.set_moments(m[:-1], v)
 
 
+def test_codes_inside_the_workspace_are_refused():
+    """They would overwrite the chunk table; nothing is launched."""
+    side = Side(specs([100_000]), 1, 1 << 20)
+    st, h, s = side.st, side.plan.handle, torch.cuda.current_stream().cuda_stream
+    m, v = torch.zeros_like(st.master), torch.zeros_like(st.master)
+    side.window(side.gradients(1))
+    before = side.state()
+    for i in range(4):
+        for at in (st.ws_ptr, st.ws_ptr + st.ws_bytes - 256):
+            coded = tuple(at if k == i else p for k, p in enumerate(st.coded))
+            for call in (lambda: B.gro_moments_encode(h, m.data_ptr(), v.data_ptr(), coded, s),
+                         lambda: B.gro_moments_decode(h, coded, m.data_ptr(), v.data_ptr(), s),
+                         lambda: B.gro_clip_adamw_coded(h, st.acc.data_ptr(), 1, 1.0, HP, 1, st.master.data_ptr(), coded,
+                                                        st.p_bf16.data_ptr(), s)):
+                with pytest.raises(B.GroError) as e:
+                    call()
+                assert e.value.kind == "invalid"
+    for flat in (m, v):
+        with pytest.raises(B.GroError):
+            B.gro_moments_decode(h, st.coded, *[st.ws_ptr if x is flat else x.data_ptr() for x in (m, v)], s)
+    torch.cuda.synchronize()
+    for got, want in zip(side.state(), before):
+        same_bits(got, want, "state")
+    side.update(1, 1.0, 1)
+
+
 def test_an_empty_plan_does_nothing():
     plan = Plan([dict(param_id=1, shape=(0,), placement="replicate")], 2, 1 << 20)
     st = DeviceState(plan, "cuda", coded_moments=True)

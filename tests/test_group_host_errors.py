@@ -8,6 +8,7 @@ import subprocess
 
 import pytest
 
+from gradient_reduction_optimizer_amd import binding as B
 from gradient_reduction_optimizer_amd import build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -38,3 +39,23 @@ def test_a_step_that_fails_midway_is_not_repeated(client):
 
 def test_a_norm_that_fails_midway_is_not_read(client):
     run(client, "norm")
+
+
+def test_a_workspace_inside_an_array_is_refused():
+    """The kernels would overwrite the table of array pointers that they
+    follow.  Refused on the host: no pointer here is one of a device."""
+    for bits8 in (False, True):
+        h = B.gro_group_create([dict(numel=100_000, coded_moments=bits8)] * 2)
+        need = B.gro_group_get_info(h)["workspace_bytes"]
+        size = [400_000, 100_000, 100_000, 6252, 6252, 200_000] if bits8 else [400_000, 400_000, 400_000, 0, 0, 200_000]
+        base = [[(1 + 6 * i + j) << 24 if size[j] else 0 for j in range(6)] for i in range(2)]
+        for i in range(2):
+            for j in range(6):
+                if not size[j]:
+                    continue
+                at, last = base[i][j], (base[i][j] + size[j] - 1) // 256 * 256
+                for ws in (at, last, at - need + 256):      # from its first byte, its last ones, up to its first ones
+                    with pytest.raises(B.GroError) as e:
+                        B.gro_group_bind(h, base, ws, need)
+                    assert e.value.kind == "duplicate", (i, j, ws)
+        B.gro_group_destroy(h)
