@@ -109,7 +109,7 @@ __global__ __launch_bounds__(kBlock) void k_group_norm(const GroupNormLaunch<N> 
 template <typename In, bool CODED, bool SPLIT>
 __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch P) {
   // last to first: the norm has just read the last gradients
-  const int64_t q = P.q_end - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
+  const int64_t q = P.q_end - 1 - (SPLIT ? int64_t(blockIdx.x / kVecsPerLane) : int64_t(blockIdx.x));
   const GroupChunkDev ch = P.chunks[q];
   const void* g = P.chunk_grads[q];
   double norm;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kBlock, 4) void k_group_adamw(const GroupStepLaunch
   const StepScalars k = step_scalars(P.k, norm, (ch.flags & kChunkDecayed) != 0);
   StepChunk c = {g, ch.p, ch.m, ch.v, ch.m_scale, ch.v_scale, ch.pb, ch.len};
   if (SPLIT) {
-    take_part<In, CODED>(c, int(blockIdx.x & 3));
+    take_part<In, CODED>(c, int(blockIdx.x % kVecsPerLane));
     if (c.len == 0) return;
   }
   const bool wide =
@@ -141,7 +141,7 @@ template <typename In, bool CODED>
 void group_step(const GroupStepLaunch& a, hipStream_t s) {
   const int64_t n = a.q_end - a.q_begin;
   if (n <= kSplitChunks)
-    hipLaunchKernelGGL((k_group_adamw<In, CODED, true>), dim3(unsigned(4 * n)), dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((k_group_adamw<In, CODED, true>), dim3(unsigned(kVecsPerLane * n)), dim3(kBlock), 0, s, a);
   else
     hipLaunchKernelGGL((k_group_adamw<In, CODED, false>), dim3(unsigned(n)), dim3(kBlock), 0, s, a);
 }

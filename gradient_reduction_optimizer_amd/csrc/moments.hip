@@ -17,7 +17,7 @@ namespace {
 template <bool NT, bool SPLIT>
 __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P) {
   // last to first, as k_adamw
-  const int64_t q = P.n_chunks - 1 - (SPLIT ? int64_t(blockIdx.x >> 2) : int64_t(blockIdx.x));
+  const int64_t q = P.n_chunks - 1 - (SPLIT ? int64_t(blockIdx.x / kVecsPerLane) : int64_t(blockIdx.x));
   const ChunkDev ch = P.chunks[q];
   if (P.scalars[kFinite] == 0.0) return;  // non-finite norm: skip the step
   const StepScalars k = step_scalars(P.k, P.scalars[kNorm], P.buckets[ch.bucket].decayed != 0);
@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P)
                  P.moments.m_scale + b, P.moments.v_scale + b,
                  P.p_bf16 ? P.p_bf16 + ch.begin : nullptr, ch.len};
   if (SPLIT) {
-    take_part<AccIn<NT>, true>(c, int(blockIdx.x & 3));
+    take_part<AccIn<NT>, true>(c, int(blockIdx.x % kVecsPerLane));
     if (c.len == 0) return;
   }
   step_chunk<AccIn<NT>, true, SPLIT>(c, k, true);
@@ -43,8 +43,8 @@ __global__ __launch_bounds__(kBlock) void k_adamw_coded(const CodedStepLaunch P)
 #ifndef GRO_DECODE_VECS
 #define GRO_DECODE_VECS 1
 #endif
-constexpr int kEncodeVecs = GRO_ENCODE_VECS;
-constexpr int kDecodeVecs = GRO_DECODE_VECS;
+constexpr int kEncodeVecs = std::min(GRO_ENCODE_VECS, kVecsPerLane);
+constexpr int kDecodeVecs = std::min(GRO_DECODE_VECS, kVecsPerLane);
 static_assert(kVecsPerLane % kEncodeVecs == 0 && kVecsPerLane % kDecodeVecs == 0, "whole workgroups per chunk");
 
 // This workgroup's stretch of a chunk: flat index of its first element, and
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kBlock) void k_moments_decode(const MomentsLaunch P
 template <bool NT>
 void adamw_coded(const CodedStepLaunch& a, hipStream_t s) {
   if (a.n_chunks <= kSplitChunks)
-    hipLaunchKernelGGL((k_adamw_coded<NT, true>), dim3(unsigned(4 * a.n_chunks)), dim3(kBlock), 0, s, a);
+    hipLaunchKernelGGL((k_adamw_coded<NT, true>), dim3(unsigned(kVecsPerLane * a.n_chunks)), dim3(kBlock), 0, s, a);
   else
     hipLaunchKernelGGL((k_adamw_coded<NT, false>), dim3(unsigned(a.n_chunks)), dim3(kBlock), 0, s, a);
 }
@@ -134,9 +134,9 @@ hipError_t launch_adamw_coded(const CodedStepLaunch& a, bool acc_nt, hipStream_t
   return hipGetLastError();
 }
 
-// A launch has fewer than 2^32 lanes: with up to four workgroups per chunk, 2^21
-// chunks (8.6e9 elements) at a time.
-constexpr int64_t kMomentsSlice = int64_t(1) << 21;
+// A launch has fewer than 2^32 lanes: with up to one for four elements, 2^33
+// elements (2^21 chunks) at a time.
+constexpr int64_t kMomentsSlice = (int64_t(1) << 33) / kChunkElems;
 static_assert(kMomentsSlice * kVecsPerLane * kBlock < (int64_t(1) << 32), "one launch's lanes");
 
 template <typename Launch>

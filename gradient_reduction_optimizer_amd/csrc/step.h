@@ -224,9 +224,9 @@ __device__ void step_any(const StepChunk& c, const StepScalars& k) {
 // bounds checks.  Every load is issued before one is used.  Same operations as
 // step_any.
 constexpr int kPartElems = 4 * kBlock;  // one vector per lane
-constexpr int kVecsPerLane = kChunkElems / kPartElems;
-static_assert(kVecsPerLane == 4 && kChunkElems == 4 * kPartElems, "a chunk is four vectors per lane");
-static_assert(kPartElems % kCodedBlock == 0, "whole blocks per quarter chunk");
+constexpr int kVecsPerLane = kChunkElems / kPartElems;  // 4 with 4096-element chunks and 256 lanes
+static_assert(kVecsPerLane >= 1 && kChunkElems == kVecsPerLane * kPartElems, "a chunk is whole vectors per lane");
+static_assert(kPartElems % kCodedBlock == 0, "whole blocks per part of a chunk");
 enum CopyMode { kNoCopy = 0, kCopy = 1, kMaybeCopy = 2 };
 
 template <typename In, bool CODED, int U, bool FULL, int WM, int COPY>
@@ -295,8 +295,8 @@ __device__ __forceinline__ void step_wide(const StepChunk& c, const StepScalars&
   }
 }
 
-// A chunk by one workgroup: all of it in one sweep of four vectors per lane.
-// SPLIT: a quarter of it, for few chunks (see kSplitChunks).
+// A chunk by one workgroup: all of it in one sweep of kVecsPerLane vectors per
+// lane.  SPLIT: one vector per lane of it, for few chunks (see kSplitChunks).
 template <typename In, bool CODED, bool SPLIT>
 __device__ __forceinline__ void step_chunk(const StepChunk& c, const StepScalars& k, bool wide) {
   if (!wide) {
@@ -314,9 +314,10 @@ __device__ __forceinline__ void step_chunk(const StepChunk& c, const StepScalars
   }
 }
 
-// Up to this many chunks a step takes four workgroups per chunk, one vector
-// per lane each, instead of one with four: few workgroups leave most of the 256
-// CUs idle, and a lane's four vectors are four times the arithmetic in a row.
+// Up to this many chunks a step takes kVecsPerLane (four) workgroups per chunk,
+// one vector per lane each, instead of one with four: few workgroups leave most
+// of the 256 CUs idle, and a lane's four vectors are four times the arithmetic
+// in a row.
 // Group steps of n full chunks, split against whole, us: n = 16, 32-bit
 // moments 3.9 / 5.3, 8-bit 5.5 / 6.4; n = 64 5.5 / 5.9 and 5.9 / 6.7; n = 128
 // 6.6 / 6.3 and 6.8 / 7.0; n = 256 8.0 / 7.7 and 8.3 / 7.7; n = 4096 78 / 78 and
@@ -326,7 +327,7 @@ __device__ __forceinline__ void step_chunk(const StepChunk& c, const StepScalars
 #endif
 constexpr int64_t kSplitChunks = GRO_SPLIT_CHUNKS;
 
-// The part of a chunk that workgroup `part` of the four takes.
+// The part of a chunk that workgroup `part` of its kVecsPerLane takes.
 template <typename In, bool CODED>
 __device__ __forceinline__ void take_part(StepChunk& c, int part) {
   const int e = part * kPartElems;
