@@ -24,7 +24,6 @@ Prints ONE JSON line.  See --help for options.
 from __future__ import annotations
 
 import argparse
-import hashlib
 import json
 import math
 import os
@@ -43,7 +42,6 @@ SHAPES = {
     "hybrid-moe-4000": "4000 tensors, lognormal sizes, 70% EP-local experts",
     "dense-8b-share": "one 1e9-element FSDP shard of an 8B dense model",
 }
-KERNEL_SRC = os.path.join(ROOT, "gradient_reduction_optimizer_amd", "csrc", "kernels.hip")
 PROFILES = os.path.join(ROOT, "profiles")  # traffic_<workload>.json: rocprofv3 byte counters
 PROBE_LIB = os.path.join(ROOT, "gradient_reduction_optimizer_amd", "libgro_probe.so")
 
@@ -82,20 +80,16 @@ def parse():
     return ap.parse_args()
 
 
-def kernel_source_hash() -> str:
-    with open(KERNEL_SRC, "rb") as f:
-        return hashlib.sha256(f.read()).hexdigest()[:16]
-
-
 def load_traffic(kernel: str, workload: str):
     """HBM traffic of `kernel` from the committed counter summary, or None if
-    missing, taken on another workload or from a different kernel source."""
+    missing, taken on another workload or from other sources of the library."""
+    from gradient_reduction_optimizer_amd.profiling import source_hash
     try:
         with open(os.path.join(PROFILES, f"traffic_{workload}.json")) as f:
             t = json.load(f)
     except (OSError, ValueError):
         return None
-    if t.get("kernel_source_sha256_16") != kernel_source_hash():
+    if t.get("source_sha256_16") != source_hash():
         return None
     if not str(t.get("workload", "")).startswith(workload + " "):
         return None

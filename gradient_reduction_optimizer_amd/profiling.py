@@ -34,7 +34,22 @@ from collections import defaultdict
 
 OURS = ("k_accumulate_window", "k_accumulate", "k_adamw_coded", "k_adamw", "k_norm_partials", "k_norm_final",
         "k_moments_encode", "k_moments_decode", "k_group_norm", "k_group_adamw")
-KERNEL_SRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc", "kernels.hip")
+CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc")
+
+
+def source_hash(csrc: str = CSRC) -> str:
+    """What ties counted bytes to the code that moved them: the library's
+    sources, every one (loads, stores and cache policies are in headers that
+    several kernels share, launches in the entry points), but for the probes,
+    which are a library of their own."""
+    h = hashlib.sha256()
+    for name in sorted(os.listdir(csrc)):
+        if name.endswith((".hip", ".h", ".cpp")) and name != "stream_probe.hip":
+            with open(os.path.join(csrc, name), "rb") as f:
+                body = f.read()
+            h.update(f"{name} {len(body)}\n".encode())
+            h.update(body)
+    return h.hexdigest()[:16]
 
 
 def short_name(name: str) -> str:
@@ -87,7 +102,7 @@ def traffic(fetch_csv: str, write_csv: str, copy_bytes: int) -> dict:
     res = {"calibration": {"copy_bytes_each_way": copy_bytes,
                            "copy_fetch_kib": sum(cf) / len(cf), "copy_write_kib": sum(cw) / len(cw),
                            "fetch_scale": scale_f, "write_scale": scale_w},
-           "kernel_source_sha256_16": hashlib.sha256(open(KERNEL_SRC, "rb").read()).hexdigest()[:16],
+           "source_sha256_16": source_hash(),
            "kernels": {}}
     for k in _ours_and_probes(f.keys()):
         if k in f and k in w:
@@ -124,7 +139,7 @@ def requests(copy_bytes: int, paths) -> dict:
             xs = sorted(xs)[-top:]
         return sum(xs) / len(xs) if xs else None
 
-    res = {"kernel_source_sha256_16": hashlib.sha256(open(KERNEL_SRC, "rb").read()).hexdigest()[:16],
+    res = {"source_sha256_16": source_hash(),
            "kernels": {}}
     for k in _ours_and_probes(v.keys()) + ["copy"]:
         top = 3 if k == "copy" else None   # the calibration copies are the largest copy dispatches

@@ -190,3 +190,31 @@ def test_probe_kernels_keep_their_template_arguments():
         "probe_window<16, 8>"
     assert P.short_name("void (anonymous namespace)::probe_adamw<4>((anonymous namespace)::Streams, long)") == \
         "probe_adamw<4>"
+
+
+@pytest.mark.parametrize("name", ["kernels.hip", "lane.h", "step.h", "coded.h", "moments.hip", "group.hip", "abi.hip"])
+def test_a_change_in_any_source_outdates_counted_bytes(tmp_path, monkeypatch, name):
+    """Loads, stores and cache policies of k_adamw are in lane.h, its launch in
+    abi.hip: bytes counted before a change there are not reported after it."""
+    import shutil
+    sys.path.insert(0, ROOT)
+    import bench
+    csrc = tmp_path / "csrc"
+    shutil.copytree(P.CSRC, csrc)
+    monkeypatch.setattr(P.source_hash, "__defaults__", (str(csrc),))
+    monkeypatch.setattr(bench, "PROFILES", str(tmp_path))
+    copy = "void at::native::elementwise_copy_kernel(...)"
+    adam = "gro::(anonymous namespace)::k_adamw(gro::AdamWLaunch)"
+    for c in ("FETCH_SIZE", "WRITE_SIZE"):
+        _counter_csv(tmp_path / f"{c}.csv", [(copy, c, 1024.0), (adam, c, 100.0)])
+    t = P.traffic(str(tmp_path / "FETCH_SIZE.csv"), str(tmp_path / "WRITE_SIZE.csv"), 1 << 20)
+    t["workload"] = "draft-67m (as counted)"
+    (tmp_path / "traffic_draft-67m.json").write_text(json.dumps(t))
+    assert bench.load_traffic("k_adamw", "draft-67m") == 200 * 1024
+    with open(csrc / "stream_probe.hip", "a") as f:
+        f.write("// not part of the library\n")
+    assert bench.load_traffic("k_adamw", "draft-67m") == 200 * 1024
+    with open(csrc / name, "a") as f:
+        f.write("// another cache policy\n")
+    assert bench.load_traffic("k_adamw", "draft-67m") is None
+    assert P.requests(1, [])["source_sha256_16"] == P.source_hash()
