@@ -358,6 +358,15 @@ int gro_init_uniform(gro_plan* plan, uint64_t seed, const double* bounds, const 
  * itself or 2^-18 of its block's largest.  An infinite v is held as the largest
  * finite one; a NaN or negative v, or a NaN or infinite m, makes that moment
  * NaN in its whole block.
+ * What rounding to the nearest code cannot follow: a step that changes a moment
+ * by less than half a code leaves it as it is.  v with beta2 of 0.97 or more
+ * and m with beta1 of 0.97 or more do not come down by decay alone: without a
+ * gradient an element keeps its code, and its moment follows its block's
+ * largest one only.  An element whose gradients become much smaller than its
+ * block's largest for good keeps too large a v and takes steps that much too
+ * small (after a tenfold fall 5 to 10 times, as long as the largest stays).
+ * Meant for gradients whose sizes within 64 neighbours keep their order;
+ * FP32 moments, which a group chooses by tensor, have no such limit.
  * In a plan a block is [64 k, 64 k + 64) of the flat arrays -- bucket bases
  * are multiples of 64, so no block spans two buckets; the part of a block past
  * the end of its bucket does not enter the scale and its bytes stay as they
