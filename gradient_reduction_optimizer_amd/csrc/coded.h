@@ -35,10 +35,11 @@ constexpr float kScaleFloor = 0x1p-100f;  // 256 / s stays far from overflow abo
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kRootMaxBits = 0x5f7fffffu;  // the largest FP32 whose square is finite: 2^64 - 2^40
 
-// 1 / x rounded to nearest: the hardware reciprocal and one Newton step.  Equal
-// to the IEEE division for every FP32 x from 2^-126 to 2^126, where the result
-// leaves the normal range (all of them compared on a gfx950), at 6 issue slots
-// -- a transcendental instruction takes 4 -- instead of 13.
+// 1 / x rounded to nearest: the hardware reciprocal and one Newton step, for x
+// from 2^-108 to 2^120 (a scale, or a scale / 256), where neither it nor the
+// remainder leaves the normal range.  Equal to the IEEE division for every
+// mantissa, tested at exponents near both ends and between them, at 6 issue
+// slots -- a transcendental instruction takes 4 -- instead of 13.
 __device__ __forceinline__ float reciprocal(float x) {
   const float y = __builtin_amdgcn_rcpf(x);
   return __builtin_fmaf(__builtin_fmaf(-x, y, 1.0f), y, y);

@@ -47,8 +47,8 @@ __device__ __forceinline__ StepScalars step_scalars(const AdamWConsts& c, double
 // round.  For v from 2^-96 to the largest finite value, which is every v of a
 // vector but in odd cases, with fewer issue slots (about 15 instead of 31):
 //   r: the hardware reciprocal root y, g = v y, r = g + (v - g^2) y/2.  Equal to
-//      the IEEE root for every FP32 in that range (all of them compared on a
-//      gfx950); below, v - g^2 would round.
+//      the IEEE root for every FP32 in that range (all of them tested); below,
+//      v - g^2 would round.
 //   q: Markstein's division by a number whose reciprocal is rounded to nearest
 //      (IBM J. Res. Dev. 34, 1990): a quotient within one step of the true one,
 //      which the first correction gives, and one more correction round to

@@ -39,7 +39,8 @@ def test_first_moments_follow_up_to_a_beta1_of_nine_tenths():
     after = decayed(codes, 1.0, M.encode_m, M.decode_m, 0.9)
     assert np.all(after[codes >= 8] < codes[codes >= 8])
     assert np.array_equal(after[:4], codes[:4]) and np.all(after[5:7] < codes[5:7])
-    assert np.array_equal(decayed(codes, 1.0, M.encode_m, M.decode_m, 0.98), codes)
+    for beta1 in (0.97, 0.99):                          # less than 1/32
+        assert np.array_equal(decayed(codes, 1.0, M.encode_m, M.decode_m, beta1), codes)
 
 
 def test_a_second_moment_stays_when_its_gradient_falls_beside_one_that_does_not():
