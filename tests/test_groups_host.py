@@ -114,3 +114,20 @@ def test_only_what_a_step_writes_counts_as_modified():
         with pytest.raises(B.GroError):
             group.clip_adamw(1.0, HP, 2)
         assert p._version == version
+
+
+def test_views_of_one_allocation_are_seen_too():
+    """They share one version counter, which a step raises whichever of them it
+    writes; a detached alias shares it as well."""
+    flat = ones(64)
+    group = TensorGroup([flat[:32], flat[32:], ones(4, 8).detach()])
+    alias = group.masters[2].detach()
+    before = flat._version, alias._version
+    grads = [ones(32, dtype=BF16), ones(32, dtype=BF16), ones(4, 8, dtype=BF16)]
+    group.norm(grads)
+    group.clip_adamw(1.0, HP, 1)
+    assert flat._version > before[0] and alias._version > before[1]
+    before = flat._version, alias._version
+    group.norm([None, grads[1], None])
+    group.clip_adamw(1.0, HP, 2)
+    assert flat._version > before[0] and alias._version == before[1]
