@@ -10,7 +10,7 @@
 // plan's (launch_norm_final).
 //
 // The step is bound by HBM: 67M elements in 34 tensors with FP32 moments move
-// 1.88 GB in 297 us (6.3 TB/s), with 8-bit moments 1.09 GB in 172 to 195 us
+// 1.88 GB in 297 us (6.3 TB/s), with 8-bit moments 1.09 GB in 165 to 195 us
 // (there the vector ALUs are close behind, and the clock decides); 299M elements
 // in 4000 tensors with 8-bit moments 4.83 GB in 808 us (6.0 TB/s).
 #include "group.h"
