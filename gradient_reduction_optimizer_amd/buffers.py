@@ -344,7 +344,12 @@ class TensorGroup:
         backward pass through a graph that saved them from before (a replay of
         a captured step does not: nothing tells autograd of it)."""
         s = self._use(stream, self._grads, self._grads_on)
-        self._call(B.gro_group_clip_adamw, max_norm, hp, step, s)
+        try:
+            self._call(B.gro_group_clip_adamw, max_norm, hp, step, s)
+        except B.GroError as e:
+            if e.code == B.GRO_E_HIP:   # some kinds of tensors may have been updated
+                self._count(self._written)
+            raise
         self._count(self._written)
         self._grads, self._grads_on, self._written = None, None, self._all
 

@@ -131,3 +131,21 @@ def test_views_of_one_allocation_are_seen_too():
     group.norm([None, grads[1], None])
     group.clip_adamw(1.0, HP, 2)
     assert flat._version > before[0] and alias._version == before[1]
+
+
+@pytest.mark.parametrize("code,counts", [(B.GRO_E_HIP, True), (B.GRO_E_STATE, False), (B.GRO_E_INVALID, False)])
+def test_a_step_that_failed_on_the_way_counts(monkeypatch, code, counts):
+    """A refused call has written nothing; a launch that failed may have left
+    other kinds of tensors updated."""
+    p = ones(4, 8)
+    group = TensorGroup([p])
+    group.norm([ones(4, 8, dtype=BF16)])
+
+    def fails(*a):
+        raise B.GroError(code, "no")
+
+    monkeypatch.setattr(B, "gro_group_clip_adamw", fails)
+    version = p._version
+    with pytest.raises(B.GroError):
+        group.clip_adamw(1.0, HP, 1)
+    assert (p._version > version) == counts
