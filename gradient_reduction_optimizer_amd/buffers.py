@@ -190,7 +190,8 @@ class TensorGroup:
     A call runs on ``stream``, by default the current one; ordering it after
     the work that made its inputs is the caller's, as with any operation on
     another stream.  Memory is not: whatever the group or the caller lets go of
-    stays as it is until the enqueued work is done with it."""
+    stays as it is until the enqueued work is done with it.  A captured graph
+    holds pointers only: group and gradients are kept as long as it is replayed."""
 
     def __init__(self, masters: Sequence, state_bits=32, no_decay=False, grad_dtype=None,
                  params_bf16: Optional[Sequence] = None, states: Optional[Sequence] = None):
