@@ -35,6 +35,10 @@ OWNER_NAMES = ("mean", "sum", "local_shard", "local_reduced", "excluded")
 GRO_MAX_NDIM = 8
 GRO_STATIC_WORKSPACE_BYTES = 16777216
 GRO_CODED_BLOCK = 64
+GRO_BF16, GRO_FP32 = 0, 1
+GRO_INT32, GRO_INT64 = 0, 1
+GRO_MAX_TABLE_ROWS = 1 << 20
+GRO_MAX_EXPERTS = 4096
 
 EXPORTS = ("gro_plan_create", "gro_plan_destroy", "gro_plan_get_info", "gro_plan_tensor",
            "gro_plan_bucket", "gro_plan_bind", "gro_plan_bind_static", "gro_accumulate", "gro_accumulate_window",
@@ -42,7 +46,9 @@ EXPORTS = ("gro_plan_create", "gro_plan_destroy", "gro_plan_get_info", "gro_plan
            "gro_reduce_norm", "gro_plan_get_norm", "gro_clip_adamw", "gro_init_uniform",
            "gro_clip_adamw_coded", "gro_moments_encode", "gro_moments_decode", "gro_group_create",
            "gro_group_destroy", "gro_group_get_info", "gro_group_bind", "gro_group_norm", "gro_group_clip_adamw",
-           "gro_group_get_norm", "gro_last_error")
+           "gro_group_get_norm", "gro_row_sort_workspace", "gro_row_sort", "gro_lookup", "gro_lookup_grad_workspace",
+           "gro_lookup_grad", "gro_experts_forward", "gro_experts_input_grad", "gro_experts_weight_grad_workspace",
+           "gro_experts_weight_grad", "gro_last_error")
 
 
 class gro_tensor_desc(ctypes.Structure):
@@ -95,6 +101,17 @@ class gro_group_tensor(ctypes.Structure):
 class gro_group_info(ctypes.Structure):
     _fields_ = [("n_tensors", ctypes.c_int32), ("chunk_elems", ctypes.c_int32), ("n_chunks", ctypes.c_int64),
                 ("n_elems", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class gro_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class gro_experts(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("outer", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("expert_stride", ctypes.c_int64), ("n_experts", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class GroError(RuntimeError):
@@ -156,6 +173,16 @@ def load() -> ctypes.CDLL:
     L.gro_group_norm.argtypes = [P, P, I32, P]
     L.gro_group_clip_adamw.argtypes = [P, D, ctypes.POINTER(gro_adamw_hparams), I64, P]
     L.gro_group_get_norm.argtypes = [P, ctypes.POINTER(D), ctypes.POINTER(D), ctypes.POINTER(I32)]
+    M, W = ctypes.POINTER(gro_matrix), ctypes.POINTER(gro_experts)
+    L.gro_row_sort_workspace.argtypes = [I64, I64, ctypes.POINTER(U64)]
+    L.gro_row_sort.argtypes = [P, I32, I64, I64, I64, P, P, P, U64, P]
+    L.gro_lookup.argtypes = [M, I64, P, I32, D, M, P]
+    L.gro_lookup_grad_workspace.argtypes = [I64, I64, ctypes.POINTER(U64)]
+    L.gro_lookup_grad.argtypes = [M, P, P, D, I32, M, P, U64, P]
+    L.gro_experts_forward.argtypes = [M, W, P, M, P]
+    L.gro_experts_input_grad.argtypes = [M, W, P, M, P]
+    L.gro_experts_weight_grad_workspace.argtypes = [I32, I64, I64, I64, ctypes.POINTER(U64)]
+    L.gro_experts_weight_grad.argtypes = [M, M, P, I32, W, P, U64, P]
     L.gro_last_error.argtypes = []
     L.gro_last_error.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -420,3 +447,52 @@ def gro_group_get_norm(group: int):
     n, sq, f = ctypes.c_double(), ctypes.c_double(), ctypes.c_int32()
     _check(load().gro_group_get_norm(group, ctypes.byref(n), ctypes.byref(sq), ctypes.byref(f)))
     return n.value, sq.value, bool(f.value)
+
+
+def _bytes(call, *args) -> int:
+    n = ctypes.c_uint64()
+    _check(call(*args, ctypes.byref(n)))
+    return n.value
+
+
+def gro_row_sort_workspace(n: int, n_rows: int) -> int:
+    return _bytes(load().gro_row_sort_workspace, n, n_rows)
+
+
+def gro_row_sort(d_ids: int, id_type: int, n: int, first_row: int, n_rows: int, d_order: int, d_starts: int,
+                 d_workspace: int = 0, nbytes: int = 0, stream: int = 0) -> None:
+    _check(load().gro_row_sort(d_ids, id_type, n, first_row, n_rows, d_order, d_starts, d_workspace, nbytes, stream))
+
+
+def gro_lookup(table: gro_matrix, first_row: int, d_ids: int, id_type: int, scale: float, out: gro_matrix,
+               stream: int = 0) -> None:
+    """table, out: ``gro_matrix(data, rows, cols, stride, type)``."""
+    _check(load().gro_lookup(table, first_row, d_ids, id_type, scale, out, stream))
+
+
+def gro_lookup_grad_workspace(n: int, cols: int) -> int:
+    return _bytes(load().gro_lookup_grad_workspace, n, cols)
+
+
+def gro_lookup_grad(dy: gro_matrix, d_order: int, d_starts: int, scale: float, accumulate: bool, out: gro_matrix,
+                    d_workspace: int = 0, nbytes: int = 0, stream: int = 0) -> None:
+    _check(load().gro_lookup_grad(dy, d_order, d_starts, scale, accumulate, out, d_workspace, nbytes, stream))
+
+
+def gro_experts_forward(x: gro_matrix, weights: gro_experts, d_starts: int, y: gro_matrix, stream: int = 0) -> None:
+    """weights: ``gro_experts(data, outer, inner, stride, expert_stride, n_experts, type)``."""
+    _check(load().gro_experts_forward(x, weights, d_starts, y, stream))
+
+
+def gro_experts_input_grad(dy: gro_matrix, weights: gro_experts, d_starts: int, dx: gro_matrix,
+                           stream: int = 0) -> None:
+    _check(load().gro_experts_input_grad(dy, weights, d_starts, dx, stream))
+
+
+def gro_experts_weight_grad_workspace(n_experts: int, rows: int, inner: int, outer: int) -> int:
+    return _bytes(load().gro_experts_weight_grad_workspace, n_experts, rows, inner, outer)
+
+
+def gro_experts_weight_grad(dy: gro_matrix, x: gro_matrix, d_starts: int, accumulate: bool, dw: gro_experts,
+                            d_workspace: int = 0, nbytes: int = 0, stream: int = 0) -> None:
+    _check(load().gro_experts_weight_grad(dy, x, d_starts, accumulate, dw, d_workspace, nbytes, stream))

@@ -158,6 +158,20 @@ class DeviceState:
             for r, g in enumerate(slot_grads):
                 bufs[b][r, dst:dst + cnt].copy_(g[src:src + cnt], non_blocking=True)
 
+    def grad_view(self, bufs: List, i: int, slot: int, shape: Optional[Sequence[int]] = None):
+        """Tensor i's contribution of one slot as a view of its bucket's buffer,
+        flat or in ``shape``, for gradients written in place.  A tensor that
+        spans several buckets has no such view: ValueError (its gradient is
+        packed, or the plan made with a larger bucket_elems)."""
+        where = self.plan.segments(i)
+        if len(where) != 1:
+            raise ValueError(f"tensor {i} lies in {len(where)} buckets, a view needs it in one")
+        b, dst, _, cnt = where[0]
+        if not 0 <= slot < bufs[b].shape[0]:
+            raise ValueError(f"slot {slot} of {bufs[b].shape[0]}")
+        flat = bufs[b][slot, dst:dst + cnt]
+        return flat if shape is None else flat.view(*shape)
+
     def flat_view(self, arr, i: int):
         """Tensor i's slice of a flat array (acc, master, m, v, p_bf16)."""
         t = self.plan.tensors[i]

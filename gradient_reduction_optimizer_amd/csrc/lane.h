@@ -112,7 +112,7 @@ __device__ __forceinline__ void st4f_acc(float* p, const f32x4 v) {
 // Sum over the workgroup in a fixed order: a wave64 butterfly (every lane
 // ends with the same bits because IEEE addition commutes), then the wave
 // totals in wave order.  Returned in every lane.
-__device__ double block_sum(double x) {
+[[maybe_unused]] __device__ double block_sum(double x) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
   __shared__ double part[kWaves];

@@ -1,0 +1,115 @@
+// The layers beside the step -- lookups with their gradient by sorted tokens
+// (rows.hip) and experts' products (experts.hip): launch arguments, and the
+// rules that host and kernels share.  Internal to the library.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+namespace gro {
+
+// A matrix as a kernel sees it: element (i, j) at at + i * stride + j.
+struct Matrix {
+  void* at;
+  int64_t rows, cols, stride;
+  int32_t fp32;             // 1: FP32, 0: BF16
+};
+
+// ------------------------------------------------------------- positions by row
+// Rows belong to buckets of 256 consecutive ones (of 1024 in tables of more than
+// 2^18 rows), which one workgroup sorts.
+constexpr int64_t kMaxTableRows = int64_t(1) << 20;
+constexpr int64_t kMaxIds = (int64_t(1) << 31) - (1 << 16);
+constexpr int kMaxBuckets = 1024;
+// Positions that one tile of a sorting workgroup holds.
+constexpr int kSortTile = 8192;
+
+inline int bucket_bits(int64_t n_rows) { return n_rows <= int64_t(kMaxBuckets) << 8 ? 8 : 10; }
+
+struct RowSortLaunch {
+  const void* ids;
+  int32_t wide_ids;         // 1: 64-bit ids
+  int64_t n;
+  int64_t first;
+  int64_t n_rows;
+  int32_t* order;
+  int32_t* starts;
+  // Workspace of the sort in several launches (n > kSortTile).
+  uint32_t* pairs;          // [n][2]: row, position
+  uint32_t* counts;         // [n_chunks][n_buckets]
+  uint32_t* bases;          // [n_buckets + 1]
+  int32_t n_chunks;
+  int32_t n_buckets;
+  int64_t chunk;            // ids per chunk, a multiple of kSortChunk
+};
+constexpr int kSortChunk = 4096;
+constexpr int64_t kMaxSortChunks = 256;
+
+inline int64_t sort_chunk(int64_t n) {
+  const int64_t tiles = (n + kSortChunk - 1) / kSortChunk;
+  return (tiles + kMaxSortChunks - 1) / kMaxSortChunks * kSortChunk;
+}
+
+hipError_t launch_row_sort(const RowSortLaunch& a, hipStream_t s);
+
+// ---------------------------------------------------------------------- lookups
+struct LookupLaunch {
+  Matrix table;
+  int64_t first;
+  const void* ids;
+  int32_t wide_ids;
+  float scale;
+  Matrix out;
+};
+hipError_t launch_lookup(const LookupLaunch& a, hipStream_t s);
+
+// Tokens in order are cut into runs of this many; a run within one row is summed
+// by the first launch.
+inline int64_t run_tokens(int64_t n) {
+  int64_t c = 16;
+  while (c * 4096 < n) c *= 2;
+  return c;
+}
+
+struct LookupGradLaunch {
+  Matrix dy;
+  const int32_t* order;
+  const int32_t* starts;
+  float scale;
+  int32_t accumulate;
+  Matrix out;
+  float* partials;          // [n / run][cols rounded up to 8]
+  int64_t run;
+  int64_t n_runs;           // whole runs, 0: no first launch
+};
+hipError_t launch_lookup_grad(const LookupGradLaunch& a, hipStream_t s);
+
+// ------------------------------------------------------------- experts' products
+// C = A B^T summed over k, for each expert: rows of A, rows of B or the k of both
+// are cut by `starts`.
+enum ExpertsMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+struct ExpertsLaunch {
+  const uint16_t* a;        // forward x, input gradient dy, weight gradient dy
+  const uint16_t* b;        // forward and input gradient W, weight gradient x
+  void* c;                  // y, dx, dW
+  int64_t a_stride, b_stride, c_stride;
+  int64_t expert_stride;    // of the weights
+  const int32_t* starts;
+  int32_t n_experts;
+  int64_t rows;             // rows that starts may name
+  int64_t inner, outer;
+  int32_t c_fp32;
+  int32_t accumulate;       // weight gradient only
+  float* partials;          // weight gradient in several parts of the rows
+  int32_t n_parts;
+};
+// The most workgroups that a call launches (a launch has fewer than 2^32 lanes).
+int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode);
+constexpr int64_t kMaxExpertsTiles = (int64_t(1) << 23) - 1;
+int weight_grad_parts(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer);
+hipError_t launch_experts(const ExpertsLaunch& a, ExpertsMode mode, hipStream_t s);
+
+}  // namespace gro

@@ -1,0 +1,237 @@
+"""The layers whose weight gradients the framework reduces: an embedding's lookup
+with its gradient by sorted tokens, and experts' matrix products over ragged runs
+of rows.  They read a step's BF16 copies and write gradients where the step reads
+them: ``DeviceState.grad_view`` is a tensor's place in a bucket buffer, and a
+``TensorGroup`` takes any of these gradients as it is.
+
+    by_row = RowOrder(tokens, 16384, 1024)                  # once
+    table = st.flat_view(st.p_bf16, i).view(16384, 1024)
+    x = lookup(table, ids, scale)
+    ...
+    by_row.sort(ids)
+    by_row.lookup_grad(dx, scale, out=st.grad_view(bufs, i, slot, (16384, 1024)))
+
+A call runs on ``stream``, by default the current one; ordering it after the work
+that made its inputs is the caller's, as with any operation on another stream.
+Memory is not: what a call uses on a stream other than the current one is kept until
+that stream is done with it.  Nothing here takes part in autograd: forward and
+gradient are calls of their own.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+_TYPES = {torch.bfloat16: B.GRO_BF16, torch.float32: B.GRO_FP32}
+_IDS = {torch.int32: B.GRO_INT32, torch.int64: B.GRO_INT64}
+
+
+def _matrix(what: str, t, device, dtypes=_TYPES) -> B.gro_matrix:
+    """A matrix of one of these types on this GPU whose rows' elements lie side by side."""
+    if t.dim() != 2 or t.dtype not in dtypes or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a matrix of {' or '.join(map(str, dtypes))} on {device}, rows' elements side by side, "
+                         f"is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    rows, cols = t.shape
+    return B.gro_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols, _TYPES[t.dtype], 0)
+
+
+def _experts(what: str, t, device, dtypes=_TYPES) -> B.gro_experts:
+    if t.dim() != 3 or t.dtype not in dtypes or t.device != device or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what}: [experts, outer, inner] of {' or '.join(map(str, dtypes))} on {device}, rows' elements side "
+                         f"by side, is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    n, outer, inner = t.shape
+    row = t.stride(1) if outer > 1 else inner
+    return B.gro_experts(t.data_ptr(), outer, inner, row, t.stride(0) if n > 1 else outer * row, n, _TYPES[t.dtype], 0)
+
+
+def _index(what: str, t, device, dtypes, n=None) -> None:
+    if t.dim() != 1 or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: {'' if n is None else f'{n} '}contiguous {' or '.join(map(str, dtypes))} on {device} are "
+                         f"needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _gpu(t) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError(f"the layers' tensors are on a GPU, got {t.device}")
+    return t.device
+
+
+def _call(device, stream, tensors, made, fn, *args) -> int:
+    """fn(..., stream handle) with the tensors' device current; returns the handle.  A stream that is not the current
+    one waits for tensors that this call has ``made`` on the current one, and the tensors it uses are recorded with the
+    allocator."""
+    here = torch.cuda.current_stream(device)
+    s = here if stream is None else stream
+    if s != here:
+        if made:
+            s.wait_stream(here)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+    handle = s.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            fn(*args, handle)
+    return handle
+
+
+def _wrote(out) -> None:
+    """An operation in place on the caller's tensor, as autograd counts them."""
+    torch.autograd.graph.increment_version(out)
+
+
+def _aligned(room) -> int:
+    return (room.data_ptr() + 255) // 256 * 256
+
+
+def _room(nbytes: int, device):
+    return torch.empty(nbytes + 256, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def lookup(table, ids, scale: float = 1.0, first_row: int = 0, out=None, dtype=None, stream=None):
+    """``scale * table[ids - first_row]`` (gro_lookup), zeros for ids of another shard of the table; ids of any
+    shape, the result has it with the table's width behind.  ``out``: a matrix of a row for each id, or one is
+    allocated in ``dtype``, by default the table's."""
+    device = _gpu(table)
+    flat = ids.contiguous().view(-1)
+    _index("ids", flat, device, _IDS)
+    if out is None:
+        rows = torch.empty((flat.numel(), table.shape[-1]), dtype=dtype or table.dtype, device=device)
+    else:
+        rows = out
+    m, o = _matrix("table", table, device), _matrix("out", rows, device)
+    if o.rows != flat.numel():
+        raise ValueError(f"out: {flat.numel()} rows are needed, got {o.rows}")
+    _call(device, stream, (table, flat, rows), out is None or flat.data_ptr() != ids.data_ptr(), B.gro_lookup, m, first_row,
+          flat.data_ptr(), _IDS[flat.dtype], scale, o)
+    if out is None:
+        return rows.view(*ids.shape, rows.shape[1])
+    _wrote(out)
+    return out
+
+
+class RowOrder:
+    """Positions sorted by the row of a table that they name, for up to ``n`` ids and a table (or a shard of one) of
+    ``n_rows``, with what ``sort`` and ``lookup_grad`` (of up to ``width`` columns) need allocated once.  ``order``
+    and ``starts`` are those of the last ``sort``: also an expert's runs of rows, for the products below, from a
+    router's choices with ``n_rows`` experts.  One sort or gradient at a time: on another stream than the last
+    call's, order it after that one."""
+
+    def __init__(self, n: int, n_rows: int, width: int = 0, device="cuda"):
+        device = torch.device(device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        self.n, self.n_rows, self.width, self.used = int(n), int(n_rows), int(width), 0
+        self._sort_bytes = B.gro_row_sort_workspace(self.n, self.n_rows)
+        self._bytes = max(self._sort_bytes, B.gro_lookup_grad_workspace(self.n, self.width))
+        self.workspace = torch.empty(self._bytes + 256, dtype=torch.uint8, device=self.device)
+        self._ws = _aligned(self.workspace)
+        self._order = torch.zeros(self.n, dtype=torch.int32, device=self.device)
+        self.starts = torch.zeros(self.n_rows + 1, dtype=torch.int32, device=self.device)
+        born = torch.cuda.current_stream(self.device)
+        born.synchronize()                  # so that any stream may be the first to use them
+        self._seen = {born.cuda_stream}     # streams that need no (further) recording of the object's own memory
+
+    @property
+    def order(self):
+        """A position for each id of the last sort; those behind ``starts[-1]`` say nothing."""
+        return self._order[:self.used]
+
+    def _run(self, stream, tensors, made, fn, *args) -> None:
+        handle = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        if handle not in self._seen:
+            s = torch.cuda.current_stream(self.device) if stream is None else stream
+            for t in (self._order, self.starts, self.workspace):
+                t.record_stream(s)
+            self._seen.add(handle)
+        _call(self.device, stream, tensors, made, fn, *args)
+
+    def sort(self, ids, first_row: int = 0, stream=None):
+        """gro_row_sort: (order, starts) of these ids, read in order of their elements."""
+        flat = ids.contiguous().view(-1)
+        _index("ids", flat, self.device, _IDS)
+        n = flat.numel()
+        if n > self.n:
+            raise ValueError(f"{n} ids, {self.n} at most")
+        self._run(stream, (flat,), flat.data_ptr() != ids.data_ptr(), B.gro_row_sort, flat.data_ptr(), _IDS[flat.dtype], n,
+                  first_row, self.n_rows, self._order.data_ptr(), self.starts.data_ptr(), self._ws, self._bytes)
+        self.used = n
+        return self.order, self.starts
+
+    def lookup_grad(self, dy, scale: float = 1.0, out=None, accumulate: bool = False, dtype=None, stream=None):
+        """gro_lookup_grad of the last sorted ids: ``out[r] = scale * sum of dy[i]`` over row r's positions, written
+        or (``accumulate``) added.  ``dy``: a row for each id.  ``out``: [n_rows, width], or one is allocated in
+        ``dtype``, by default dy's."""
+        if dy.dim() < 2:
+            raise ValueError(f"dy: a row for each id is needed, got {tuple(dy.shape)}")
+        flat = dy if dy.dim() == 2 else dy.reshape(-1, dy.shape[-1])
+        d = _matrix("dy", flat, self.device)
+        if accumulate and out is None:
+            raise ValueError("accumulate adds to an array that is given")
+        given = out is not None
+        if not given:
+            out = torch.empty((self.n_rows, flat.shape[1]), dtype=dtype or flat.dtype, device=self.device)
+        o = _matrix("out", out, self.device)
+        if d.rows != self.used or o.rows != self.n_rows or d.cols > self.width:
+            raise ValueError(f"{self.used} ids were sorted for {self.n_rows} rows of up to {self.width} elements, got "
+                             f"dy {tuple(dy.shape)} and out {tuple(out.shape)}")
+        self._run(stream, (flat, out), not given or flat.data_ptr() != dy.data_ptr(), B.gro_lookup_grad, d,
+                  self._order.data_ptr(), self.starts.data_ptr(), scale, bool(accumulate), o, self._ws, self._bytes)
+        if given:
+            _wrote(out)
+        return out
+
+
+_BF16 = {torch.bfloat16: B.GRO_BF16}
+_I32 = {torch.int32: B.GRO_INT32}
+
+
+def _product(fn, in_name, rows, weight, starts, out, out_name, cols, dtype, stream):
+    device = _gpu(rows)
+    w = _experts("weight", weight, device, _BF16)
+    _index("starts", starts, device, _I32, w.n_experts + 1)
+    given = out is not None
+    if not given:  # rows that no expert has are not written by the product
+        out = torch.zeros((rows.shape[0], getattr(w, cols)), dtype=dtype or rows.dtype, device=device)
+    x, y = _matrix(in_name, rows, device, _BF16), _matrix(out_name, out, device)
+    _call(device, stream, (rows, weight, starts, out), not given, fn, x, w, starts.data_ptr(), y)
+    if given:
+        _wrote(out)
+    return out
+
+
+def experts_forward(x, weight, starts, out=None, dtype=None, stream=None):
+    """y = x W_e^T for the rows ``starts[e]:starts[e + 1]`` of each expert (gro_experts_forward).  ``x`` [rows, inner] and
+    ``weight`` [experts, outer, inner] BF16, ``starts`` int32 on the GPU, ``out`` [rows, outer] BF16 or FP32; one of
+    zeros is allocated in ``dtype``, by default BF16, when it is not given.  Rows of no expert stay as they were."""
+    return _product(B.gro_experts_forward, "x", x, weight, starts, out, "y", "outer", dtype, stream)
+
+
+def experts_input_grad(dy, weight, starts, out=None, dtype=None, stream=None):
+    """dx = dy W_e (gro_experts_input_grad); ``dy`` [rows, outer], ``out`` [rows, inner], else as experts_forward."""
+    return _product(B.gro_experts_input_grad, "dy", dy, weight, starts, out, "dx", "inner", dtype, stream)
+
+
+def experts_weight_grad(dy, x, starts, out=None, accumulate: bool = False, dtype=None, stream=None):
+    """dW_e = dy^T x over each expert's rows (gro_experts_weight_grad), written or (``accumulate``) added; zeros, or
+    what was there, for an expert without rows.  ``out`` [experts, outer, inner] BF16 or FP32, or one is allocated in
+    ``dtype``, by default BF16."""
+    device = _gpu(dy)
+    d, r = _matrix("dy", dy, device, _BF16), _matrix("x", x, device, _BF16)
+    _index("starts", starts, device, _I32)
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to an array that is given")
+    given = out is not None
+    if not given:
+        out = torch.empty((max(starts.numel() - 1, 0), d.cols, r.cols), dtype=dtype or dy.dtype, device=device)
+    w = _experts("out", out, device)
+    _index("starts", starts, device, _I32, w.n_experts + 1)
+    nbytes = B.gro_experts_weight_grad_workspace(w.n_experts, d.rows, w.inner, w.outer)
+    room = _room(nbytes, device)
+    _call(device, stream, (dy, x, starts, out, room), not given or room is not None, B.gro_experts_weight_grad, d, r,
+          starts.data_ptr(), bool(accumulate), w, _aligned(room) if nbytes else 0, nbytes)
+    if given:
+        _wrote(out)
+    return out

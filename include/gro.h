@@ -34,7 +34,8 @@
  *    BF16 parameter copy, the per-bucket gradient buffers and the workspace).
  *    The library never allocates or frees device memory and never calls a
  *    collective.  A plan owns only host tables.
- *  - Device pointers must be 16-byte aligned (256-byte for the workspace).
+ *  - Device pointers must be 16-byte aligned (256-byte for the workspace); a
+ *    group's and the layers' arrays only to their element.
  *  - Streams: `stream` is a hipStream_t passed as void* (NULL = the null
  *    stream).  All device work is enqueued on it, asynchronously.  Use one
  *    stream per plan, or per group, at a time.
@@ -46,7 +47,8 @@
  *    gro_plan_get_norm, gro_group_bind and gro_group_get_norm wait for the
  *    device.  The step's calls (gro_accumulate*, gro_reduce_norm,
  *    gro_clip_adamw, gro_clip_adamw_coded, gro_moments_encode,
- *    gro_moments_decode, gro_group_norm, gro_group_clip_adamw) only enqueue kernels
+ *    gro_moments_decode, gro_group_norm, gro_group_clip_adamw) and the layers'
+ *    (gro_row_sort, gro_lookup*, gro_experts_*) only enqueue kernels
  *    -- no allocation, no synchronization, no memory fill -- so a step may be
  *    captured in a HIP graph after binding and replayed; the replay repeats
  *    the captured arguments, the AdamW step count included.
@@ -477,6 +479,103 @@ int gro_group_clip_adamw(gro_group* group, double max_norm, const gro_adamw_hpar
 /* Wait for the stream of the last gro_group_norm and read its norm, as
  * gro_plan_get_norm. */
 int gro_group_get_norm(gro_group* group, double* norm, double* norm_sq, int32_t* finite);
+
+/* ---- layers: what makes the gradients of an embedding and of experts ----
+ * A model's embedding and its experts' matrices are parameters like the others;
+ * these calls are their forward passes, which read the BF16 copy that a step
+ * leaves, and their gradients, written where gro_accumulate or gro_group_norm
+ * reads them (a slot of a bucket, a gradient of a group).  Nothing is kept between
+ * calls.  Sums are FP32 in an order that depends on the sizes, the rows' lengths
+ * and the starts alone, never on timing: a call repeated gives the same bits.
+ * Calls on different streams may overlap if each has a workspace of its own.  No
+ * call waits, allocates or fills memory by a copy engine: all may be captured.
+ * Arrays may lie at any address that is aligned to their element; outputs must not
+ * overlap inputs or the workspace (columns side by side in one matrix do not). */
+#define GRO_BF16 0
+#define GRO_FP32 1
+#define GRO_INT32 0
+#define GRO_INT64 1
+
+/* A matrix in device memory: element (i, j) is data[i * stride + j].  stride >=
+ * cols where there is more than one row.  data may be NULL without elements. */
+typedef struct gro_matrix {
+  void* data;
+  int64_t rows;
+  int64_t cols;
+  int64_t stride;
+  int32_t type;             /* GRO_BF16 or GRO_FP32 */
+  int32_t reserved;         /* 0 */
+} gro_matrix;
+
+/* Rows that a table of the calls below has at most (2^20). */
+#define GRO_MAX_TABLE_ROWS 1048576
+
+/* Positions by the row they name: the ids id[0..n) of a table shard that holds the
+ * rows first_row .. first_row + n_rows - 1 of the whole table.  d_order[0..m): the m
+ * positions whose id is one of them, by row and within a row ascending; what lies
+ * behind stays as it was.  d_starts[r] (n_rows + 1 entries): where row r's positions
+ * begin, d_starts[n_rows] = m.  Ids of other shards, negative ones and any other
+ * values are left out.  Also gives experts' runs of rows: ids = a router's choices,
+ * n_rows = the number of experts.
+ * d_ids: GRO_INT32 or GRO_INT64 (id_type); n < 2^31 - 2^16.  The workspace (256-byte
+ * aligned) has the bytes that gro_row_sort_workspace gives, 0 for short lists. */
+int gro_row_sort_workspace(int64_t n, int64_t n_rows, uint64_t* bytes);
+int gro_row_sort(const void* d_ids, int32_t id_type, int64_t n, int64_t first_row, int64_t n_rows,
+                 int32_t* d_order, int32_t* d_starts, void* d_workspace, uint64_t bytes, void* stream);
+
+/* out[i, :] = scale * table[id[i] - first_row, :], multiplied in FP32 and rounded
+ * once; zeros where the id is none of the table's (another shard's: the shards'
+ * results add up to the whole).  out->rows ids.  Table and out are BF16 or FP32
+ * each.  The scale is rounded to FP32. */
+int gro_lookup(const gro_matrix* table, int64_t first_row, const void* d_ids, int32_t id_type, double scale,
+               const gro_matrix* out, void* stream);
+
+/* The lookup's gradient from sorted positions (gro_row_sort of the same ids, with
+ * n = dy->rows and n_rows = out->rows): out[r, :] = scale * sum of dy[i, :] over row
+ * r's positions i.  Every row is written, zeros for rows without any; with
+ * accumulate = 1 it is added to what is there, and rows without any are not touched
+ * (a tied head's gradient, an FP32 gradient of several microbatches).  Sums are
+ * FP32, rounded once.  dy and out are BF16 or FP32 each.  Entries of d_order and
+ * d_starts outside their range are never followed. */
+int gro_lookup_grad_workspace(int64_t n, int64_t cols, uint64_t* bytes);
+int gro_lookup_grad(const gro_matrix* dy, const int32_t* d_order, const int32_t* d_starts, double scale,
+                    int32_t accumulate, const gro_matrix* out, void* d_workspace, uint64_t bytes, void* stream);
+
+/* Experts' matrices W_e, [outer][inner] each: element (o, i) of expert e is
+ * data[e * expert_stride + o * stride + i]. */
+typedef struct gro_experts {
+  void* data;
+  int64_t outer;
+  int64_t inner;
+  int64_t stride;
+  int64_t expert_stride;
+  int32_t n_experts;        /* at most GRO_MAX_EXPERTS */
+  int32_t type;             /* GRO_BF16, gradients GRO_BF16 or GRO_FP32 */
+  int32_t reserved;         /* 0 */
+} gro_experts;
+#define GRO_MAX_EXPERTS 4096
+
+/* Products of ragged runs of rows, each with its expert's matrix: rows d_starts[e]
+ * .. d_starts[e + 1] - 1 are expert e's (n_experts + 1 entries, not descending;
+ * entries are cut to 0 .. rows).  The runs' lengths are read on the device only.
+ *   forward:      y = x W_e^T    x [rows][inner], y [rows][outer]
+ *   input grad:   dx = dy W_e    dy [rows][outer], dx [rows][inner]
+ *   weight grad:  dW_e = dy^T x  over the expert's rows; zeros for an expert without
+ *                 rows; with accumulate = 1 added to what is there, and experts
+ *                 without rows are not touched.
+ * x, dy and W are BF16, results BF16 or FP32; products are summed in FP32 and rounded
+ * once.  Rows in front of d_starts[0] and from d_starts[n_experts] on are neither
+ * read nor written.  An expert's result depends on its own rows alone: infinities and
+ * NaN of other rows do not reach it. */
+int gro_experts_forward(const gro_matrix* x, const gro_experts* weights, const int32_t* d_starts,
+                        const gro_matrix* y, void* stream);
+int gro_experts_input_grad(const gro_matrix* dy, const gro_experts* weights, const int32_t* d_starts,
+                           const gro_matrix* dx, void* stream);
+int gro_experts_weight_grad_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer,
+                                      uint64_t* bytes);
+int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x, const int32_t* d_starts,
+                            int32_t accumulate, const gro_experts* dw, void* d_workspace, uint64_t bytes,
+                            void* stream);
 
 /* Thread-local text of the last error ("" if none). */
 const char* gro_last_error(void);

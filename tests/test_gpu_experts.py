@@ -1,0 +1,304 @@
+"""GPU: experts' products over ragged runs of rows against plain 64-bit ones:
+each direction and result type, runs of no, one and many rows, sizes around tiles,
+strides, alignments, rows of no expert, infinities and NaN of other rows, one expert,
+many experts, captured graphs, and the layers together with a plan's step."""
+import numpy as np
+import pytest
+import torch
+
+import layers_reference as R
+from gradient_reduction_optimizer_amd import binding as B
+from gradient_reduction_optimizer_amd import layers as L
+
+pytestmark = pytest.mark.gpu
+BF16, F32, F64 = R.BF16, R.F32, R.F64
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(gpu):
+    torch.cuda.synchronize()
+    yield
+    torch.cuda.synchronize()
+
+
+def normal(seed, *shape):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g).to(BF16)
+
+
+# rows of each expert, rows in front of the first and behind the last, inner, outer
+CASES = {
+    "one row": ([1], 0, 0, 64, 64),
+    "nothing": ([0, 0], 0, 3, 64, 64),
+    "no experts": ([], 0, 4, 32, 32),
+    "single tokens": ([1, 0, 2, 0, 0, 1, 3], 0, 0, 256, 512),
+    "token of a wide expert": ([0, 1, 0, 1], 0, 0, 1024, 1024),
+    "small odd": ([3, 0, 17, 5], 2, 6, 33, 31),
+    "eights": ([5, 64, 0, 129, 9], 0, 8, 72, 200),
+    "around tiles": ([63, 64, 65, 1, 0, 127, 128, 129], 1, 1, 128, 192),
+    "large tiles": ([255, 256, 257, 0, 513], 0, 0, 320, 512),
+    "wide": ([700, 20], 0, 5, 1032, 776),
+    "one long": ([3000], 7, 0, 192, 264),
+    "odd and long": ([1500, 0, 1000], 0, 0, 131, 257),
+    "no inner": ([4, 2], 0, 1, 0, 24),
+    "no outer": ([4, 2], 0, 1, 24, 0),
+    "thin": ([100, 30], 0, 0, 1, 1),
+    "many experts": ([(7 * i) % 5 for i in range(200)], 3, 3, 64, 40),
+    "batch": ([300, 500, 0, 800, 250], 0, 50, 512, 1024),
+}
+LAYOUTS = [(0, 0), (8, 0), (64, 8), (3, 1), (0, 5)]
+
+
+class Case:
+    def __init__(self, name, seed=0):
+        sizes, self.front, self.behind, self.inner, self.outer = CASES[name]
+        self.n = len(sizes)
+        self.starts = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32) + self.front
+        self.rows = int(self.starts[-1]) + self.behind
+        self.x, self.dy = normal(seed + 1, self.rows, self.inner), normal(seed + 2, self.rows, self.outer)
+        self.w = normal(seed + 3, self.n, self.outer, self.inner)
+        # what lies outside every expert must not matter
+        for t in (self.x, self.dy):
+            t[:self.front], t[self.rows - self.behind:] = float("nan"), float("inf")
+        self.dstarts = torch.from_numpy(self.starts).cuda()
+
+    def runs(self):
+        return [(e, slice(int(self.starts[e]), int(self.starts[e + 1]))) for e in range(self.n)]
+
+
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("direction", ["forward", "input"])
+def test_products_of_rows(name, direction):
+    c = Case(name)
+    src, width = (c.x, c.outer) if direction == "forward" else (c.dy, c.inner)
+    want, slack = torch.zeros(c.rows, width, dtype=F64), torch.zeros(c.rows, width, dtype=F64)
+    for e, at in c.runs():
+        want[at], slack[at] = R.product(src[at], c.w[e].t() if direction == "forward" else c.w[e])
+    call = L.experts_forward if direction == "forward" else L.experts_input_grad
+    inside = torch.zeros(c.rows, dtype=torch.bool)
+    inside[c.front:c.rows - c.behind] = True
+    for k, (pad, shift) in enumerate(LAYOUTS):
+        dtype = (BF16, F32)[k % 2]
+        s, w = R.Matrix(src, pad, shift), R.Matrix(c.w, pad, shift)
+        was = torch.full((c.rows, width), 7.0, dtype=dtype)
+        out = R.Matrix(was, pad, shift)
+        assert call(s.view, w.view, c.dstarts, out=out.view) is out.view
+        R.check_close(out.view.cpu()[inside], want[inside], slack[inside], (name, pad, shift, dtype))
+        assert bool((out.view.cpu()[~inside] == 7).all()), "rows of no expert"
+        assert out.rest_untouched()
+    got = call(src.cuda(), c.w.cuda(), c.dstarts, dtype=F32)
+    R.check_close(got.cpu()[inside], want[inside], slack[inside], (name, "allocated"))
+    assert bool((got.cpu()[~inside] == 0).all())
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_weight_gradients(name):
+    c = Case(name, 10)
+    want, slack = (torch.zeros(c.n, c.outer, c.inner, dtype=F64) for _ in "ws")
+    for e, at in c.runs():
+        want[e], slack[e] = R.product(c.dy[at].t(), c.x[at])
+    empty = torch.from_numpy(np.diff(c.starts) == 0)
+    for k, (pad, shift) in enumerate(LAYOUTS):
+        d, x = R.Matrix(c.dy, pad, shift), R.Matrix(c.x, (pad + 8) % 72, shift)
+        for dtype in (BF16, F32):
+            was = normal(k, c.n, c.outer, c.inner).to(dtype)
+            out = R.Matrix(was, pad, shift)
+            L.experts_weight_grad(d.view, x.view, c.dstarts, out=out.view)
+            R.check_close(out.view, want, slack, (name, pad, shift, dtype))
+            first = R.bits(out.view)
+            assert out.rest_untouched()
+            out = R.Matrix(was, pad, shift)
+            L.experts_weight_grad(d.view, x.view, c.dstarts, out=out.view, accumulate=True)
+            R.check_close(out.view, want + was.to(F64), slack + (want.abs() + was.to(F64).abs()) * 2.0 ** -23, (name, "added"))
+            assert torch.equal(R.bits(out.view.cpu()[empty]), R.bits(was[empty])) and out.rest_untouched()
+            again = L.experts_weight_grad(d.view, x.view, c.dstarts, dtype=dtype)
+            assert torch.equal(R.bits(again), first), "another sum on the same inputs"
+
+
+def test_infinities_and_nan_of_other_rows_do_not_arrive():
+    """Rows of an expert's neighbours share tiles with its own."""
+    c = Case("around tiles", 20)
+    for bad in range(c.n):
+        at = slice(int(c.starts[bad]), int(c.starts[bad + 1]))
+        x, dy = c.x.clone(), c.dy.clone()
+        x[at], dy[at] = float("nan"), float("inf")
+        w = c.w.clone()
+        w[bad] = float("nan")
+        y = L.experts_forward(x.cuda(), w.cuda(), c.dstarts)
+        dx = L.experts_input_grad(dy.cuda(), w.cuda(), c.dstarts)
+        dw = L.experts_weight_grad(dy.cuda(), x.cuda(), c.dstarts)
+        keep = torch.ones(c.rows, dtype=torch.bool)
+        keep[at] = False
+        keep[:c.front], keep[c.rows - c.behind:] = False, False
+        assert bool(y.cpu()[keep].isfinite().all()) and bool(dx.cpu()[keep].isfinite().all())
+        others = [e for e in range(c.n) if e != bad]
+        assert bool(dw.cpu()[others].isfinite().all())
+
+
+def test_starts_out_of_range_are_cut():
+    """Runs that leave the rows or go backwards are cut to what exists."""
+    x, w = normal(1, 100, 64).cuda(), normal(2, 4, 64, 64).cuda()
+    starts = torch.tensor([-5, 40, 30, 2 ** 31 - 1, -7], dtype=torch.int32).cuda()
+    y = L.experts_forward(x, w, starts, dtype=F32)
+    runs = [(0, 0, 40), (2, 30, 100)]       # expert 1 goes backwards, 3 begins at the end
+    for e, lo, hi in runs[1:]:
+        want, slack = R.product(x[lo:hi], w[e].t())
+        R.check_close(y[40:], want[10:], slack[10:], e)
+    dw = L.experts_weight_grad(x, x, starts, dtype=F32)
+    for e, lo, hi in runs:
+        want, slack = R.product(x[lo:hi].t(), x[lo:hi])
+        R.check_close(dw[e], want, slack, ("dw", e))
+    assert bool((dw[1] == 0).all()) and bool((dw[3] == 0).all())
+
+
+def test_columns_side_by_side_in_one_matrix():
+    """Input and result as two halves of one matrix's columns, weights as the halves of each expert's rows."""
+    c = Case("eights")
+    both = torch.zeros(c.rows, c.inner + c.outer, dtype=BF16).cuda()
+    both[:, :c.inner] = c.x.cuda()
+    pair = torch.zeros(c.n, 2 * c.outer, c.inner, dtype=BF16).cuda()
+    pair[:, c.outer:] = c.w.cuda()
+    L.experts_forward(both[:, :c.inner], pair[:, c.outer:], c.dstarts, out=both[:, c.inner:])
+    want = L.experts_forward(c.x.cuda(), c.w.cuda(), c.dstarts)
+    keep = slice(c.front, c.rows - c.behind)
+    assert torch.equal(R.bits(both[keep, c.inner:]), R.bits(want[keep]))
+    dw = torch.zeros(c.n, 2 * c.outer, c.inner).cuda()
+    L.experts_weight_grad(c.dy.cuda(), c.x.cuda(), c.dstarts, out=dw[:, c.outer:])
+    assert bool((dw[:, :c.outer] == 0).all())
+    assert torch.equal(dw[:, c.outer:], L.experts_weight_grad(c.dy.cuda(), c.x.cuda(), c.dstarts, dtype=F32))
+
+
+def test_gradients_against_differences():
+    """d sum(y * r) along a direction, by the forward product at two points: y is linear in x and in W, so the
+    difference over any distance is the gradient's product with the direction."""
+    c = Case("eights", 30)
+    keep = slice(c.front, c.rows - c.behind)
+    x, w, r = c.x.clone(), c.w.clone(), c.dy.clone()
+    for t in (x, r):
+        t[c.rows - c.behind:] = 0
+    x, w, r = x.cuda(), w.cuda(), r.cuda()
+    dx = L.experts_input_grad(r, w, c.dstarts, dtype=F32).double()
+    dw = L.experts_weight_grad(r, x, c.dstarts, dtype=F32).double()
+    f = lambda x, w: (L.experts_forward(x, w, c.dstarts, dtype=F32).double()[keep] * r.double()[keep]).sum()  # noqa: E731
+    # steps of whole powers of two on values of few bits stay exact in BF16
+    ex, ew = torch.randint(-1, 2, x.shape).to(BF16).cuda(), torch.randint(-1, 2, w.shape).to(BF16).cuda()
+    x0, w0 = (t.float().mul(4).round().div(4).to(BF16) for t in (x, w))
+    dx0 = L.experts_input_grad(r, w0, c.dstarts, dtype=F32).double()
+    dw0 = L.experts_weight_grad(r, x0, c.dstarts, dtype=F32).double()
+    scale = float((x0.double().abs().max() + 1) * (w0.double().abs().max() + 1) * r.double().abs().sum() * c.inner)
+    for got, change in (((f(x0 + ex, w0) - f(x0 - ex, w0)) / 2, (dx0 * ex.double())[keep].sum()),
+                        ((f(x0, w0 + ew) - f(x0, w0 - ew)) / 2, (dw0 * ew.double()).sum())):
+        assert abs(float(got - change)) <= scale * (c.inner + c.outer) * 2.0 ** -23
+    assert dx.shape == x.shape and dw.shape == w.shape
+
+
+def test_captured_and_replayed():
+    """Runs' lengths are read on the device: a replay follows the starts of its time."""
+    c = Case("batch", 40)
+    x, dy, w = c.x.cuda().nan_to_num(0, 0, 0), c.dy.cuda().nan_to_num(0, 0, 0), c.w.cuda()
+    starts = c.dstarts.clone()
+    y, dx, dw = torch.zeros_like(dy), torch.zeros_like(x), torch.zeros(w.shape, device="cuda")
+
+    def step():
+        L.experts_forward(x, w, starts, out=y)
+        L.experts_input_grad(dy, w, starts, out=dx)
+        L.experts_weight_grad(dy, x, starts, out=dw, accumulate=True)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k, sizes in enumerate(([300, 500, 0, 800, 250], [0, 0, 0, 0, 1900], [1, 2, 3, 4, 5], [380] * 5)):
+        starts.copy_(torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32))
+        x.copy_(normal(50 + k, *x.shape))
+        got = []
+        for run in (graph.replay, step):
+            for t in (y, dx, dw):
+                t.fill_(0.5)
+            run()
+            torch.cuda.synchronize()
+            got.append([t.clone() for t in (y, dx, dw)])
+        assert all(torch.equal(R.bits(a), R.bits(b)) for a, b in zip(*got)), sizes
+
+
+def test_two_streams_at_once():
+    """Calls that overlap, each with results and workspace of its own."""
+    c = Case("batch", 60)
+    x, dy, w = c.x.cuda().nan_to_num(0, 0, 0), c.dy.cuda().nan_to_num(0, 0, 0), c.w.cuda()
+    want = [L.experts_forward(x, w, c.dstarts), L.experts_weight_grad(dy, x, c.dstarts, dtype=F32)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    got = [[L.experts_forward(x, w, c.dstarts, stream=s), L.experts_weight_grad(dy, x, c.dstarts, dtype=F32, stream=s)]
+           for _ in range(5) for s in streams]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(R.bits(a), R.bits(b)) for a, b in zip(pair, want))
+
+
+def test_an_embedding_and_experts_through_a_step():
+    """One microbatch of a small model through the layers into a plan's buckets and its step, as a user runs it:
+    the gradients arrive where gro_accumulate reads them, and the BF16 copies that the step leaves are read next."""
+    from gradient_reduction_optimizer_amd.buffers import DeviceState, Plan
+    V, H, F, E, T, K = 300, 64, 128, 6, 500, 2
+    plan = Plan([dict(param_id=0, shape=(V, H), placement="shard", shard_index=0),
+                 dict(param_id=1, shape=(E, F, H), placement="shard", shard_index=0),
+                 dict(param_id=2, shape=(E, H, F), placement="shard", shard_index=0, fp32_grad=True)], 2, 1 << 20)
+    st = DeviceState(plan, "cuda")
+    shapes = [(V, H), (E, F, H), (E, H, F)]
+    for i, s in enumerate(shapes):
+        st.flat_view(st.master, i).copy_(normal(i, *s).float().reshape(-1).cuda() * 0.1)
+    st.p_bf16.copy_(st.master)
+    bufs = st.grad_buffers()
+    by_token, by_expert = L.RowOrder(T, V, H), L.RowOrder(T * K, E)
+    by_source = L.RowOrder(T * K, T, H)
+    hp = dict(lr=1e-2, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
+    s = torch.cuda.current_stream().cuda_stream
+    for step in (1, 2):
+        r = np.random.default_rng(step)
+        tokens = torch.from_numpy(r.integers(0, V, T)).cuda()
+        choice = torch.from_numpy(np.stack([r.permutation(E)[:K] for _ in range(T)])).to(torch.int32).cuda()
+        emb, up, down = (st.flat_view(st.p_bf16, i).view(*q) for i, q in enumerate(shapes))
+        h = L.lookup(emb, tokens, 8.0)
+        order, starts = by_expert.sort(choice)
+        source = (order // K).to(torch.int32)               # the token of each row of the experts
+        x = L.lookup(h, source)
+        a = L.experts_forward(x, up, starts)
+        y = L.experts_forward(a, down, starts)
+        dy = (y.float() * 1e-2).to(BF16)                    # of the loss 0.005 * sum(y^2)
+        da = L.experts_input_grad(dy, down, starts)
+        dx = L.experts_input_grad(da, up, starts)
+        L.experts_weight_grad(dy, a, starts, out=st.grad_view(bufs, 2, 0, shapes[2]))
+        L.experts_weight_grad(da, x, starts, out=st.grad_view(bufs, 1, 0, shapes[1]))
+        by_source.sort(source)
+        dh = by_source.lookup_grad(dx)
+        by_token.sort(tokens)
+        by_token.lookup_grad(dh, 8.0, out=st.grad_view(bufs, 0, 0, (V, H)))
+
+        # the same in 64 bits from the same copies
+        p = [t.detach().double().cpu().requires_grad_() for t in (emb, up, down)]
+        hh = p[0][tokens.cpu()] * 8.0
+        loss = 0
+        for t in range(K):
+            e = choice[:, t].cpu().long()
+            v = torch.bmm(p[2][e], torch.bmm(p[1][e], hh[:, :, None]))
+            loss = loss + 0.005 * v.square().sum()
+        loss.backward()
+        for i, q in enumerate(p):
+            got = st.grad_view(bufs, i, 0, shapes[i]).double().cpu()
+            # five BF16 roundings in a row at most (h, a, y, dy, da, dx, dh: seven), each 2^-8 of its value, and
+            # sums of them: in norm no more than their sum
+            off = float((got - q.grad).norm() / q.grad.norm())
+            assert off <= 8 * 2.0 ** -8, (step, i, off)
+        B.gro_accumulate(plan.handle, 0, plan.info["n_buckets"], [b.data_ptr() for b in bufs], st.acc.data_ptr(), 0, 1, s)
+        B.gro_reduce_norm(plan.handle, st.acc.data_ptr(), 1, s)
+        norm, _, finite = B.gro_plan_get_norm(plan.handle)
+        want = float(sum(q.grad.square().sum() for q in p)) ** 0.5
+        assert finite and abs(norm - want) <= 8 * 2.0 ** -8 * want
+        before = st.p_bf16.clone()
+        B.gro_clip_adamw(plan.handle, st.acc.data_ptr(), 1, 1.0, hp, step, st.master.data_ptr(), st.m.data_ptr(),
+                         st.v.data_ptr(), st.p_bf16.data_ptr(), s)
+        assert not torch.equal(before, st.p_bf16)
