@@ -15,42 +15,90 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Rows of expert e, cut to those that exist.
 struct Run {
-  int64_t lo, hi;
+  int lo, hi;
 };
 __device__ __forceinline__ Run run_of(const ExpertsLaunch& P, int e) {
   Run r;
-  r.lo = std::min(std::max(int64_t(P.starts[e]), int64_t(0)), P.rows);
-  r.hi = std::min(std::max(int64_t(P.starts[e + 1]), r.lo), P.rows);
+  const int rows = int(P.rows);
+  r.lo = std::min(std::max(P.starts[e], 0), rows);
+  r.hi = std::min(std::max(P.starts[e + 1], r.lo), rows);
   return r;
 }
 
-// The expert and the first row of this workgroup's tile of BM rows: tiles are
-// numbered expert by expert.  False behind the last one.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x)))) |
+                 uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x >> 32)))) << 32);
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Which of `total` tiles is workgroup b's, of tiles numbered so that `chunk` in a row
+// are neighbours.  Workgroup b runs on XCD b mod 8: each XCD takes a chunk at a time, so
+// that tiles which read the same rows and columns of the operands at the same time
+// share its L2.  `total` or more: none.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total, uint32_t chunk) {
+  const uint32_t c = std::min(chunk, (total + 7) / 8), j = b >> 3;
+  return c > 0 ? (j / c * 8 + (b & 7)) * c + j % c : 0;
+}
+// Numbers b that reach every tile so.
+__host__ __device__ inline uint32_t xcd_numbers(uint32_t total, uint32_t chunk) { return (total + 7) / 8 * 8 + 8 * chunk; }
+
+// Number `i` of a grid of m_tiles x n_tiles in bands of up to 8 tiles of m: neighbours
+// in number are neighbours in both.
+struct Place {
+  uint32_t m, n;
+};
+__device__ __forceinline__ Place banded(uint32_t i, uint32_t m_tiles, uint32_t n_tiles) {
+  const uint32_t band = i / (8 * n_tiles), in_band = std::min(8u, m_tiles - 8 * band), r = i - band * 8 * n_tiles;
+  return Place{band * 8 + r % in_band, r / in_band};
+}
+
+// Tiles of BM rows that the experts' runs take, and of one of them the expert and its
+// rows: tiles are numbered expert by expert.  A wave looks at 64 experts at a time.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const ExpertsLaunch& P, int64_t tile, int& expert, int64_t& row, int64_t& end) {
-  const int lane = int(threadIdx.x) & 63;
-  for (int e0 = 0; e0 < P.n_experts; e0 += 64) {
-    Run r = {0, 0};
-    if (e0 + lane < P.n_experts) r = run_of(P, e0 + lane);
-    const int64_t mine = (r.hi - r.lo + BM - 1) / BM;
-    int64_t upto = mine;
+struct Tiles {
+  Run r;            // lane's expert of the first 64
+  uint32_t upto;
+  uint32_t total;
+  static __device__ __forceinline__ uint32_t count(const Run& r) { return uint32_t(r.hi - r.lo + BM - 1) / BM; }
+  static __device__ __forceinline__ Run run(const ExpertsLaunch& P, int e) {
+    return e < P.n_experts ? run_of(P, e) : Run{0, 0};
+  }
+  static __device__ __forceinline__ uint32_t prefix(uint32_t x) {
+    const int lane = int(threadIdx.x) & 63;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-      const int64_t t = __shfl_up(upto, m, 64);
-      if (lane >= m) upto += t;
+      const uint32_t t = __shfl_up(x, m, 64);
+      if (lane >= m) x += t;
     }
-    const uint64_t over = __ballot(upto > tile);
-    if (over) {
-      const int l = __ffsll(static_cast<unsigned long long>(over)) - 1;
-      expert = e0 + l;
-      row = __shfl(r.lo, l, 64) + (tile - __shfl(upto - mine, l, 64)) * BM;
-      end = __shfl(r.hi, l, 64);
-      return true;
-    }
-    tile -= __shfl(upto, 63, 64);
+    return x;
   }
-  return false;
-}
+  __device__ __forceinline__ Tiles(const ExpertsLaunch& P) {
+    const int lane = int(threadIdx.x) & 63;
+    r = run(P, lane);
+    upto = prefix(count(r));
+    total = uint32_t(__builtin_amdgcn_readlane(int(upto), 63));
+    for (int e0 = 64; e0 < P.n_experts; e0 += 64)
+      total += uint32_t(__builtin_amdgcn_readlane(int(prefix(count(run(P, e0 + lane)))), 63));
+  }
+  __device__ __forceinline__ void find(const ExpertsLaunch& P, uint32_t tile, int& expert, int& row, int& end) const {
+    const int lane = int(threadIdx.x) & 63;
+    Run q = r;
+    uint32_t u = upto;
+    for (int e0 = 0;; e0 += 64) {
+      const uint64_t over = __ballot(u > tile);
+      if (over) {
+        const int l = uniform(__ffsll(static_cast<unsigned long long>(over)) - 1);
+        expert = e0 + l;
+        row = __builtin_amdgcn_readlane(q.lo + int(tile - (u - count(q))) * BM, l);
+        end = __builtin_amdgcn_readlane(q.hi, l);
+        return;
+      }
+      tile -= uint32_t(__builtin_amdgcn_readlane(int(u), 63));
+      q = run(P, e0 + 64 + lane);
+      u = prefix(count(q));
+    }
+  }
+};
 
 // ------------------------------------------------------------ any sizes, simply
 // 64 x 64 of C by four waves of 32 x 32, k in steps of 32, elements staged one by
@@ -74,7 +122,12 @@ __global__ __launch_bounds__(256) void k_experts_simple(const ExpertsLaunch P) {
     k_hi = r.hi;
     if (P.accumulate && r.lo == r.hi) return;
   } else {
-    if (!find_tile<kSimple>(P, tile, expert, m0, m_end)) return;
+    const Tiles<kSimple> tiles(P);
+    if (tile >= tiles.total) return;
+    int row, end;
+    tiles.find(P, uint32_t(tile), expert, row, end);
+    m0 = row;
+    m_end = end;
     k_hi = MODE == kForward ? P.inner : P.outer;
   }
   const uint16_t* b = P.b + (MODE == kWeightGrad ? 0 : int64_t(expert) * P.expert_stride);
@@ -130,151 +183,157 @@ __global__ __launch_bounds__(256) void k_experts_simple(const ExpertsLaunch P) {
 // ------------------------------------------------- full tiles, straight to LDS
 // BM x BN of C by WM x WN waves, k in steps of 64.  Both operands' tiles are copied
 // from global memory to LDS without passing registers, into one of two buffers while
-// the matrix cores work on the other; every wave reads the second half of a step's
-// fragments while it multiplies the first, and the next step's first half while it
-// multiplies the second, so one barrier a step is all that it waits for.
+// the matrix cores work on the other; every wave reads the fragments of a quarter of a
+// step while it multiplies those of the quarter before, so one barrier a step is all
+// that it waits for.  A workgroup goes from tile to tile: the next one's first two steps
+// are under way while this one's result is written, through LDS, in whole lines.
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define GRO_LDS __attribute__((address_space(3)))
-#define GRO_GLOBAL __attribute__((address_space(1)))
-constexpr int kStepK = 64;
+constexpr int kStepK = 32, kStages = 4;
+// LDS of a workgroup: two steps of both operands, and for each wave a block of 32 x 32
+// results.
+constexpr int tile_lds(int bm, int bn, int waves) { return (bm + bn) * kStepK * 2 * kStages + waves * 32 * 32 * 4; }
+// Workgroups of a compute unit, and tiles that an XCD's 32 units work on at a time.
+constexpr int tile_units(int bm, int bn, int waves) { return 160 * 1024 / tile_lds(bm, bn, waves); }
 
 // One operand's tile of R rows (of C) and 64 k.
 //   k innermost in memory (T = false): LDS holds [R][64], row r's chunk c of 8
-//   elements at place c ^ (r & 7), so that 8 rows' reads of one chunk meet all banks.
+//   elements at place c ^ (r / 2 mod 8), so that 16 rows' reads of one chunk meet all
+//   banks.
 //   rows of C innermost (T = true): LDS holds [64][R], unit u of 16 elements of k at
-//   place u ^ (k & 3 | k >> 1 & 4); fragments come out of transposing reads, whose 16
-//   k of an instruction then meet all banks.
+//   place u ^ (k & 3 | k >> 1 & 4); fragments come out of transposing reads, whose
+//   8 different k meet all banks.
 template <bool T, int R, int THREADS>
 struct Tile {
   static constexpr int kChunks = T ? R / 8 : kStepK / 8;       // of a line in LDS
-  static constexpr int kLines = T ? kStepK : R;
   static constexpr int kLoads = R * kStepK / 8 / THREADS;      // 16 bytes each, of a lane
   static constexpr int kLineStep = THREADS / kChunks;          // lines between a lane's loads
-  static_assert(kLineStep % 16 == 0, "a lane's lines have one swizzle");
 
-  // What a lane copies: its first line and the chunk that belongs to its place in it.
-  static __device__ __forceinline__ int line() { return int(threadIdx.x) / kChunks; }
-  static __device__ __forceinline__ int chunk() {
-    const int c = int(threadIdx.x) % kChunks, l = line();
-    return T ? c ^ (((l & 3) | ((l >> 1) & 4)) << 1) : c ^ (l & 7);
+  // What a lane copies in load i: its line and the chunk that belongs to its place there.
+  static __device__ __forceinline__ int line(int i) { return int(threadIdx.x) / kChunks + i * kLineStep; }
+  static __device__ __forceinline__ int chunk(int i) {
+    const int c = int(threadIdx.x) % kChunks, l = line(i);
+    return T ? c ^ (((l & 3) | ((l >> 1) & 4)) << 1) : c ^ ((l >> 2) & 3);
   }
 };
 
-__device__ __forceinline__ void copy_to_lds(const uint16_t* from, uint16_t* to) {
-  __builtin_amdgcn_global_load_lds((const GRO_GLOBAL void*)from, (GRO_LDS void*)to, 16, 0, 0);
-}
-
-// Loader of one operand: pointers of the lane's lines in the tile's first step.
+// Loader of one operand: where the lane's lines of a step lie, as a byte offset each
+// from an address that all lanes share.
 template <bool T, int R, int THREADS>
 struct Loader {
   typedef Tile<T, R, THREADS> L;
-  const uint16_t* from;
-  int64_t stride;
-  uint32_t at[L::kLoads];      // elements from `from` on
+  const char* from;
+  int step_bytes;              // T only
+  uint32_t at[L::kLoads];
 
-  // rows [r0, end) of the operand (lines, or columns where T); those behind read one
+  // Rows [r0, end) of the operand (lines, or columns where T); those behind read one
   // that exists, and what becomes of them is not stored.
-  __device__ __forceinline__ void set(const uint16_t* base, int64_t step, int64_t r0, int64_t end) {
-    stride = step;
-    if constexpr (T) {
-      const int64_t c = r0 + 8 * L::chunk();
-      from = base;
+  __device__ __forceinline__ void set(const uint16_t* base, int64_t stride, int r0, int end) {
+    if constexpr (T) step_bytes = uniform(2 * kStepK * int(stride));
+    from = reinterpret_cast<const char*>(uniform(int64_t(reinterpret_cast<uintptr_t>(base + (T ? r0 : r0 * stride)))));
+    const int left = end - r0, s = int(stride);
 #pragma unroll
-      for (int i = 0; i < L::kLoads; ++i)
-        at[i] = uint32_t((L::line() + i * L::kLineStep) * step + (c < end ? c : 0));
-    } else {
-      from = base + r0 * step;
-#pragma unroll
-      for (int i = 0; i < L::kLoads; ++i) {
-        const int64_t r = std::min<int64_t>(L::line() + i * L::kLineStep, end - 1 - r0);
-        at[i] = uint32_t(r * step + 8 * L::chunk());
-      }
+    for (int i = 0; i < L::kLoads; ++i) {
+      const int line = L::line(i), c = 8 * L::chunk(i);
+      at[i] = 2u * uint32_t(T ? line * s + (c < left ? c : 0) : std::min(line, left - 1) * s + c);
     }
   }
-  __device__ __forceinline__ void copy(uint16_t* lds) const {
-    uint16_t* to = lds + (threadIdx.x & ~63u) * 8;
+  __device__ __forceinline__ void copy(uint16_t* lds, int wave) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know the descriptor's type
+    const auto all = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, -1, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) copy_to_lds(from + at[i], to + i * THREADS * 8);
+    for (int i = 0; i < L::kLoads; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(all, (GRO_LDS void*)(lds + wave * 512 + i * THREADS * 8), 16, at[i], 0, 0, 0);
+#endif
+    from += T ? step_bytes : 2 * kStepK;
   }
   // A step of `left` < 64 k: zeros behind them.
   __device__ __forceinline__ void copy_part(uint16_t* lds, int left) const {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
       u16x8 x = {};
-      const uint16_t* p = from + at[i];
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(from + at[i]);
       if constexpr (T) {
-        if (L::line() + i * L::kLineStep < left) x = *reinterpret_cast<const u16x8*>(p);
+        if (L::line(i) < left) x = *reinterpret_cast<const u16x8*>(p);
       } else {
-        const int n = left - 8 * L::chunk();
+        const int n = left - 8 * L::chunk(i);
         if (n >= 8) {
           x = *reinterpret_cast<const u16x8*>(p);
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n) x[e] = p[e];
+          for (int e = 0; e < n; ++e) x[e] = p[e];
         }
       }
       *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = x;
     }
   }
-  __device__ __forceinline__ void next() { from += T ? kStepK * stride : int64_t(kStepK); }
 };
 
-// N fragments of 16 rows from row `first` of a tile on, for 32 of its k.
+// N fragments of 32 rows from row `first` of a tile on, for 16 of its k: lane l has row
+// l mod 32 and 8 k from 8 * (l / 32) on.
 template <bool T, int R, int N>
 struct Reader {
   int at[T ? N : 2];
   __device__ __forceinline__ void set(int first) {
-    const int lane = int(threadIdx.x) & 63, g = lane >> 4, l = lane & 15;
+    const int lane = int(threadIdx.x) & 63, l = lane & 15;
     if constexpr (T) {
-      const int f = (l >> 2) | ((g & 1) << 2);
+      // 16 lanes' reads give each the four k of one of 16 rows
+      const int k = 8 * (lane >> 5) + (l >> 2), f = (l >> 2) | ((lane >> 5) << 2);
 #pragma unroll
-      for (int i = 0; i < N; ++i) at[i] = (8 * g + (l >> 2)) * R + (((first / 16 + i) ^ f) * 16) + (l & 3) * 4;
+      for (int i = 0; i < N; ++i) at[i] = k * R + ((first / 16 + 2 * i + ((lane >> 4) & 1)) ^ f) * 16 + (l & 3) * 4;
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) at[h] = (first + l) * kStepK + ((4 * h + g) ^ (l & 7)) * 8;
+      for (int q = 0; q < 2; ++q)
+        at[q] = (first + (lane & 31)) * kStepK + ((2 * q + (lane >> 5)) ^ ((lane >> 2) & 3)) * 8;
     }
   }
-  // fragments [FROM, FROM + M)
-  template <int FROM, int M>
-  __device__ __forceinline__ void read(const uint16_t* lds, int half, bf16x8 (&f)[M]) const {
+  __device__ __forceinline__ void read(const uint16_t* lds, int q, bf16x8 (&f)[N]) const {
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int i = FROM + m;
+    for (int i = 0; i < N; ++i) {
       if constexpr (T) {
-        const uint16_t* p = lds + at[i] + half * 32 * R;
+        const uint16_t* p = lds + at[i] + q * 16 * R;
         const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((GRO_LDS bf16x4*)(p));
         const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((GRO_LDS bf16x4*)(p + 4 * R));
-        f[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        f[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
       } else {
-        f[m] = *reinterpret_cast<const bf16x8*>(lds + at[half] + i * 16 * kStepK);
+        f[i] = *reinterpret_cast<const bf16x8*>(lds + at[q] + i * 32 * kStepK);
       }
     }
   }
 };
 
-// Everything copied and read so far has arrived, for all waves.
-__device__ __forceinline__ void step_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All that this wave has read from LDS has arrived and all of its accesses to global
+// memory but the last N are done, for all waves.
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+  // the builtin for LDS, so that the compiler knows and adds no waits of its own behind it
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
-// Four neighbours of a row of C.
-template <bool CF>
-__device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int64_t left, f32x4 x) {
-  struct __attribute__((packed, aligned(4))) F4 { f32x4 v; };
-  struct __attribute__((packed, aligned(2))) B4 { u32x2 v; };
-  if (left >= 4) {
+// N neighbours of a row of C, of which `left` exist: four FP32 or eight BF16, 16 bytes.
+template <bool CF, int N>
+__device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int left, const float (&x)[N]) {
+  typedef f32x4 F4 __attribute__((aligned(4)));
+  typedef u16x8 B8 __attribute__((aligned(2)));
+  if (left >= N) {
     if constexpr (CF) {
       F4* c = reinterpret_cast<F4*>(static_cast<float*>(P.c) + at);
-      if (P.accumulate) x += c->v;
-      c->v = x;
+      f32x4 y = {x[0], x[1], x[2], x[3]};
+      if (P.accumulate) y += *c;
+      __builtin_nontemporal_store(y, c);
     } else {
-      B4* c = reinterpret_cast<B4*>(static_cast<uint16_t*>(P.c) + at);
-      if (P.accumulate) x += widen4(c->v);
-      c->v = u32x2{bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
+      B8* c = reinterpret_cast<B8*>(static_cast<uint16_t*>(P.c) + at);
+      u16x8 y = {};
+      if (P.accumulate) y = *c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = bf16_bits(P.accumulate ? widen1(y[e]) + x[e] : x[e]);
+      __builtin_nontemporal_store(y, c);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < N; ++e)
       if (e < left) {
         if constexpr (CF) {
           float* c = static_cast<float*>(P.c) + at + e;
@@ -287,103 +346,231 @@ __device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int6
   }
 }
 
+// The compiler's order of what stands in front of it: MFMAS matrix instructions with
+// READS reads from LDS among them, so that the wait for what the part before has read
+// stands in front of the new reads.
+template <int READS, int MFMAS>
+__device__ __forceinline__ void interleave() {
+  constexpr int kEach = (READS + MFMAS - 3) / (MFMAS - 2);
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+#pragma unroll
+  for (int i = 0; i < READS; i += kEach) {
+    __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's accesses to its own LDS in the order of the source.
+__device__ __forceinline__ void in_wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A tile of C: rows [m0, m_end) and columns from n0 on of an expert's, and the k it sums.
+struct Job {
+  int expert, m0, m_end, n0, k_lo, k_n;
+};
+
 template <int MODE, int BM, int BN, int WM, int WN, bool CF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const ExpertsLaunch P) {
-  constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 16, FN = BN / WN / 16;
+  constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
-  __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK], a1[BM * kStepK], b0[BN * kStepK], b1[BN * kStepK];
-  int expert;
-  int64_t m0, m_end, k_lo = 0, k_n;
-  const int64_t n_end = MODE == kForward ? P.outer : P.inner, n_tiles = (n_end + BN - 1) / BN;
-  const int64_t n0 = int64_t(blockIdx.x) % n_tiles * BN, tile = int64_t(blockIdx.x) / n_tiles;
-  if constexpr (MODE == kWeightGrad) {
-    const int64_t m_tiles = (P.outer + BM - 1) / BM;
-    expert = int(tile / m_tiles);
-    const Run r = run_of(P, expert);
-    m0 = tile % m_tiles * BM;
-    m_end = P.outer;
-    k_lo = r.lo;
-    k_n = r.hi - r.lo;
-    if (P.accumulate && k_n == 0) return;
-  } else {
-    if (!find_tile<BM>(P, tile, expert, m0, m_end)) return;
-    k_n = MODE == kForward ? P.inner : P.outer;
-  }
-  const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
+  constexpr uint32_t kChunk = 32 * tile_units(BM, BN, WM * WN), kGrid = 8 * kChunk;
+  __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK], a1[BM * kStepK], a2[BM * kStepK], a3[BM * kStepK];
+  __shared__ __attribute__((aligned(16))) uint16_t b0[BN * kStepK], b1[BN * kStepK], b2[BN * kStepK], b3[BN * kStepK];
+  __shared__ __attribute__((aligned(16))) float results[WM * WN][32 * 32];
+  const int n_end = int(MODE == kForward ? P.outer : P.inner);
+  const uint32_t n_tiles = uint32_t((n_end + BN - 1) / BN);
+  const int wave = uniform(int(threadIdx.x) >> 6), lane = int(threadIdx.x) & 63;
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+
+  const Tiles<BM> tiles(P);
+  const uint32_t m_tiles = MODE == kWeightGrad ? uint32_t((P.outer + BM - 1) / BM) : tiles.total;
+  const uint32_t total = m_tiles * n_tiles * (MODE == kWeightGrad ? uint32_t(P.n_experts) : 1u);
+  // weight gradients: experts with more rows first, of the first 64
+  int rank = 0;
+  if constexpr (MODE == kWeightGrad) {
+    const int mine = tiles.r.hi - tiles.r.lo;
+    for (int e = 0; e < std::min(P.n_experts, 64); ++e) {
+      const int n = __builtin_amdgcn_readlane(mine, e);
+      rank += n > mine || (n == mine && e < lane);
+    }
+  }
+  const auto by_length = [&](int place) {
+    return place < 64 ? uniform(__ffsll(static_cast<unsigned long long>(__ballot(rank == place && lane < P.n_experts))) - 1) : place;
+  };
+  // where a round of workgroups has tiles of several experts, every other round goes
+  // backwards, so that a workgroup's jobs are long and short
+  const bool turn = MODE == kWeightGrad && m_tiles * n_tiles < kGrid;
+  const auto find = [&](uint32_t b, Job& job) {
+    const uint32_t round = b / kGrid, in_round = b % kGrid;
+    const uint32_t i = xcd_order(turn && (round & 1) ? round * kGrid + (kGrid - 1 - in_round) : b, total, kChunk);
+    if (i >= total) return false;
+    if constexpr (MODE == kWeightGrad) {
+      const Place p = banded(i % (m_tiles * n_tiles), m_tiles, n_tiles);
+      job.expert = by_length(int(i / (m_tiles * n_tiles)));
+      const Run r = run_of(P, job.expert);
+      job.m0 = int(p.m) * BM;
+      job.n0 = int(p.n) * BN;
+      job.m_end = int(P.outer);
+      job.k_lo = uniform(r.lo);
+      job.k_n = uniform(r.hi - r.lo);
+    } else {
+      const Place p = banded(i, m_tiles, n_tiles);
+      tiles.find(P, p.m, job.expert, job.m0, job.m_end);
+      job.n0 = int(p.n) * BN;
+      job.k_lo = 0;
+      job.k_n = int(MODE == kForward ? P.inner : P.outer);
+    }
+    return true;
+  };
+  // the next tile that a workgroup has, of those xcd_order leaves it
+  uint32_t b = blockIdx.x;
+  const uint32_t last = (xcd_numbers(total, kChunk) + kGrid - 1) / kGrid * kGrid;
+  const auto next = [&](Job& job) {
+    for (; b < last; b += kGrid)
+      if (find(b, job)) {
+        b += kGrid;
+        return true;
+      }
+    return false;
+  };
+
+  constexpr int kWide = CF ? 4 : 8, kLanes = 32 / kWide, kRows = 64 / kLanes;
   Loader<AT, BM, kThreads> la;
   Loader<BT, BN, kThreads> lb;
-  la.set(P.a + (AT ? k_lo * P.a_stride : 0), P.a_stride, m0, m_end);
-  lb.set(P.b + (MODE == kWeightGrad ? k_lo * P.b_stride : int64_t(expert) * P.expert_stride), P.b_stride, n0, n_end);
+  constexpr int kLoads = decltype(la)::L::kLoads + decltype(lb)::L::kLoads, kStores = FM * FN * 32 / kRows;
+  static_assert((kStages - 1) * kLoads + kStores < 64, "vmcnt counts to 63");
   Reader<AT, BM, FM> ra;
   Reader<BT, BN, FN> rb;
   ra.set(wm);
   rb.set(wn);
-  const int steps = int((k_n + kStepK - 1) / kStepK);
-  const auto load = [&](int step, uint16_t* a, uint16_t* b) {
-    const int64_t left = k_n - int64_t(step) * kStepK;
-    if (left >= kStepK) {
-      la.copy(a);
-      lb.copy(b);
-    } else {
-      la.copy_part(a, int(left));
-      lb.copy_part(b, int(left));
-    }
-    la.next();
-    lb.next();
+  uint16_t* const as[kStages] = {a0, a1, a2, a3};
+  uint16_t* const bs[kStages] = {b0, b1, b2, b3};
+  const auto load = [&](int stage) {
+    la.copy(as[stage], wave);
+    lb.copy(bs[stage], wave);
   };
-  f32x4 acc[FM][FN] = {};
-  // A step in four parts: two halves of its k, and of each the lower and the upper half
-  // of the rows.
-  constexpr int kHalf = FM / 2;
-  bf16x8 fa[2][kHalf], fb[2][FN];
-  const auto multiply = [&](auto upper, const bf16x8 (&x)[kHalf], const bf16x8 (&y)[FN]) {
+  const auto begin = [&](const Job& job) {
+    la.set(P.a + (AT ? job.k_lo * P.a_stride : 0), P.a_stride, job.m0, job.m_end);
+    lb.set(P.b + (MODE == kWeightGrad ? job.k_lo * P.b_stride : job.expert * P.expert_stride), P.b_stride, job.n0, n_end);
 #pragma unroll
-    for (int i = 0; i < kHalf; ++i)
+    for (int t = 0; t < kStages; ++t)
+      if (job.k_n >= (t + 1) * kStepK) load(t);
+  };
+
+  Job job;
+  if (!next(job)) return;
+  begin(job);
+  bool stored = false;  // kStores stores by every wave since the next job's first loads
+  for (bool more = true; more;) {
+    Job ahead;               // found while the first loads are under way
+    more = next(ahead);
+    f32x16 acc[FM][FN] = {};
+    // A step in two parts of 16 k.
+    constexpr int kPart = FM * FN, kReads = FM * (AT ? 2 : 1) + FN * (BT ? 2 : 1);
+    bf16x8 fa[2][FM], fb[2][FN];
+    const auto read = [&](int stage, int q) {
+      ra.read(as[stage], q, fa[q]);
+      rb.read(bs[stage], q, fb[q]);
+    };
+    const auto multiply = [&](int q) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q][j], fa[q][i], acc[i][j], 0, 0, 0);
+    };
+    const int steps = job.k_n / kStepK, left = job.k_n % kStepK;
+    // step s has been loaded kStages - 1 steps ago; behind its loads are those of two more
+    const auto step = [&](int s, auto number) {
+      constexpr int kStage = decltype(number)::value;
+      read(kStage, 1);
+      multiply(0);
+      interleave<kReads, kPart>();
+      if (s + kStages <= steps) {
+        if (stored && s < kStages - 1) step_barrier<(kStages - 2) * kLoads + kStores>();
+        else step_barrier<(kStages - 2) * kLoads>();
+      } else {
+        step_barrier<0>();
+      }
+      if (s + kStages < steps) load(kStage);
+      read((kStage + 1) % kStages, 0);  // behind the last step, whatever the buffers hold
+      multiply(1);
+      interleave<kReads, kPart>();
+    };
+    if (steps > 0) {
+      if (steps >= kStages) {
+        if (stored) step_barrier<(kStages - 1) * kLoads + kStores>();
+        else step_barrier<(kStages - 1) * kLoads>();
+      } else {
+        step_barrier<0>();
+      }
+      read(0, 0);
+      for (int s = 0;;) {
+        step(s, std::integral_constant<int, 0>());
+        if (++s >= steps) break;
+        step(s, std::integral_constant<int, 1>());
+        if (++s >= steps) break;
+        step(s, std::integral_constant<int, 2>());
+        if (++s >= steps) break;
+        step(s, std::integral_constant<int, 3>());
+        if (++s >= steps) break;
+      }
+    }
+    step_barrier<0>();
+    if (left > 0) {
+      la.copy_part(a0, left);
+      lb.copy_part(b0, left);
+      step_barrier<0>();
+      read(0, 0);
+      multiply(0);
+      read(0, 1);
+      multiply(1);
+      step_barrier<0>();
+    }
+    const Job done = job;
+    job = ahead;
+    if (more) begin(job);
+    stored = done.m0 + BM <= done.m_end && done.n0 + BN <= n_end;
+
+    // Lane l has row l mod 32 of a block of C and of its columns four times four, 8 q +
+    // 4 * (l / 32) on.  32 x 32 at a time go through the wave's own LDS, row r's chunk c of
+    // four at place c ^ (r / 2 mod 8), and from there to memory in pieces of whole rows.
+    if (MODE == kWeightGrad && P.accumulate && done.k_n == 0) {
+      stored = false;
+      continue;
+    }
+    const int64_t base = MODE == kWeightGrad ? done.expert * P.expert_stride : 0;
+    float* block = results[wave];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        f32x4& c = acc[decltype(upper)::value * kHalf + i][j];
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(y[j], x[i], c, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = lane & 31, c = (2 * q + (lane >> 5)) ^ ((r >> 1) & 7);
+          st4f(block + r * 32 + 4 * c,
+               f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
+        }
+        in_wave_order();
+        const int n = done.n0 + wn + 32 * j + lane % kLanes * kWide;
+#pragma unroll
+        for (int t = 0; t < 32; t += kRows) {
+          const int r = t + lane / kLanes, m = done.m0 + wm + 32 * i + r;
+          float x[kWide];
+#pragma unroll
+          for (int h = 0; h < kWide / 4; ++h) {
+            const f32x4 v = ld4f(block + r * 32 + 4 * ((lane % kLanes * (kWide / 4) + h) ^ ((r >> 1) & 7)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+          }
+          if (m < done.m_end && n < n_end) store_c<CF, kWide>(P, base + m * P.c_stride + n, n_end - n, x);
+        }
+        in_wave_order();
       }
-  };
-  constexpr std::integral_constant<int, 0> lower{};
-  constexpr std::integral_constant<int, 1> upper{};
-  const auto step = [&](int s, uint16_t* a, uint16_t* b, const uint16_t* next_a, const uint16_t* next_b) {
-    ra.template read<kHalf, kHalf>(a, 0, fa[1]);
-    multiply(lower, fa[0], fb[0]);
-    ra.template read<0, kHalf>(a, 1, fa[0]);
-    rb.template read<0, FN>(b, 1, fb[1]);
-    multiply(upper, fa[1], fb[0]);
-    ra.template read<kHalf, kHalf>(a, 1, fa[1]);
-    multiply(lower, fa[0], fb[1]);
-    step_barrier();
-    if (s + 2 < steps) load(s + 2, a, b);
-    // behind the last step, whatever the buffers hold
-    ra.template read<0, kHalf>(next_a, 0, fa[0]);
-    rb.template read<0, FN>(next_b, 0, fb[0]);
-    multiply(upper, fa[1], fb[1]);
-  };
-  if (steps > 0) {
-    load(0, a0, b0);
-    if (steps > 1) load(1, a1, b1);
-    step_barrier();
-    ra.template read<0, kHalf>(a0, 0, fa[0]);
-    rb.template read<0, FN>(b0, 0, fb[0]);
-    for (int s = 0; s < steps; s += 2) {
-      step(s, a0, b0, a1, b1);
-      if (s + 1 < steps) step(s + 1, a1, b1, a0, b0);
-    }
-  }
-  const int64_t base = MODE == kWeightGrad ? int64_t(expert) * P.expert_stride : 0;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + wm + 16 * i + (lane & 15);
-    if (m >= m_end) continue;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
-      if (n < n_end) store_c<CF>(P, base + m * P.c_stride + n, n_end - n, acc[i][j]);
-    }
   }
 }
 
@@ -398,7 +585,7 @@ int64_t tiles_of(const ExpertsLaunch& a, ExpertsMode mode, int64_t bm, int64_t b
 // places, and a tile's offsets in 32 bits.
 bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
   const auto fits = [](const void* p, int64_t stride) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && stride < (int64_t(1) << 23);
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && stride < (int64_t(1) << 22);
   };
   if (!fits(a.a, a.a_stride) || !fits(a.b, a.b_stride) || a.expert_stride % 8 != 0) return false;
   // an operand whose rows of C lie innermost is copied 8 of them at a time
@@ -407,7 +594,9 @@ bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
 
 template <int MODE, int BM, int BN, int WM, int WN>
 hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
-  const dim3 grid(unsigned(tiles_of(a, ExpertsMode(MODE), BM, BN))), block(64 * WM * WN);
+  constexpr uint32_t units = tile_units(BM, BN, WM * WN);
+  const uint32_t n = xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
+  const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
   if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, true>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, false>), grid, block, 0, s, a);
   return hipGetLastError();
