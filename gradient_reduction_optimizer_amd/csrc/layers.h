@@ -18,15 +18,17 @@ struct Matrix {
 };
 
 // ------------------------------------------------------------- positions by row
-// Rows belong to buckets of 256 consecutive ones (of 1024 in tables of more than
-// 2^18 rows), which one workgroup sorts.
+// Rows belong to buckets of 64, 256 or 1024 consecutive ones, which one workgroup
+// sorts: as few rows as give up to 256 or kMaxBuckets buckets.
 constexpr int64_t kMaxTableRows = int64_t(1) << 20;
 constexpr int64_t kMaxIds = (int64_t(1) << 31) - (1 << 16);
 constexpr int kMaxBuckets = 1024;
 // Positions that one tile of a sorting workgroup holds.
 constexpr int kSortTile = 8192;
 
-inline int bucket_bits(int64_t n_rows) { return n_rows <= int64_t(kMaxBuckets) << 8 ? 8 : 10; }
+inline int bucket_bits(int64_t n_rows) {
+  return n_rows <= int64_t(256) << 6 ? 6 : n_rows <= int64_t(kMaxBuckets) << 8 ? 8 : 10;
+}
 
 struct RowSortLaunch {
   const void* ids;
