@@ -100,87 +100,7 @@ struct Tiles {
   }
 };
 
-// ------------------------------------------------------------ any sizes, simply
-// 64 x 64 of C by four waves of 32 x 32, k in steps of 32, elements staged one by
-// one through LDS with k innermost.
-constexpr int kSimple = 64, kSimpleK = 32;
-
-template <int MODE, bool CF>
-__global__ __launch_bounds__(256) void k_experts_simple(const ExpertsLaunch P) {
-  __shared__ uint16_t as[kSimple][kSimpleK + 8], bs[kSimple][kSimpleK + 8];
-  int expert;
-  int64_t m0, m_end, k_lo = 0, k_hi;
-  const int64_t n_end = MODE == kForward ? P.outer : P.inner, n_tiles = (n_end + kSimple - 1) / kSimple;
-  const int64_t n0 = int64_t(blockIdx.x) % n_tiles * kSimple, tile = int64_t(blockIdx.x) / n_tiles;
-  if constexpr (MODE == kWeightGrad) {
-    const int64_t m_tiles = (P.outer + kSimple - 1) / kSimple;
-    expert = int(tile / m_tiles);
-    const Run r = run_of(P, expert);
-    m0 = tile % m_tiles * kSimple;
-    m_end = P.outer;
-    k_lo = r.lo;
-    k_hi = r.hi;
-    if (P.accumulate && r.lo == r.hi) return;
-  } else {
-    const Tiles<kSimple> tiles(P);
-    if (tile >= tiles.total) return;
-    int row, end;
-    tiles.find(P, uint32_t(tile), expert, row, end);
-    m0 = row;
-    m_end = end;
-    k_hi = MODE == kForward ? P.inner : P.outer;
-  }
-  const uint16_t* b = P.b + (MODE == kWeightGrad ? 0 : int64_t(expert) * P.expert_stride);
-  const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  f32x4 acc[2][2] = {};
-  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kSimpleK) {
-    for (int i = int(threadIdx.x); i < kSimple * kSimpleK; i += 256) {
-      // lanes next to each other read neighbours in memory
-      const int am = MODE == kWeightGrad ? i % kSimple : i / kSimpleK, ak = MODE == kWeightGrad ? i / kSimple : i % kSimpleK;
-      const int bn = MODE == kForward ? i / kSimpleK : i % kSimple, bk = MODE == kForward ? i % kSimpleK : i / kSimple;
-      uint16_t x = 0, y = 0;
-      if (m0 + am < m_end && k0 + ak < k_hi)
-        x = MODE == kWeightGrad ? P.a[(k0 + ak) * P.a_stride + m0 + am] : P.a[(m0 + am) * P.a_stride + k0 + ak];
-      if (n0 + bn < n_end && k0 + bk < k_hi)
-        y = MODE == kForward ? b[(n0 + bn) * P.b_stride + k0 + bk] : b[(k0 + bk) * P.b_stride + n0 + bn];
-      as[am][ak] = x;
-      bs[bn][bk] = y;
-    }
-    __syncthreads();
-    bf16x8 fa[2], fb[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      fa[t] = *reinterpret_cast<const bf16x8*>(&as[wm + 16 * t + (lane & 15)][8 * (lane >> 4)]);
-      fb[t] = *reinterpret_cast<const bf16x8*>(&bs[wn + 16 * t + (lane & 15)][8 * (lane >> 4)]);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t m = m0 + wm + 16 * i + 4 * (lane >> 4) + e, n = n0 + wn + 16 * j + (lane & 15);
-        if (m >= m_end || n >= n_end) continue;
-        const int64_t at = (MODE == kWeightGrad ? int64_t(expert) * P.expert_stride : 0) + m * P.c_stride + n;
-        float x = acc[i][j][e];
-        if constexpr (CF) {
-          float* c = static_cast<float*>(P.c) + at;
-          *c = P.accumulate ? *c + x : x;
-        } else {
-          uint16_t* c = static_cast<uint16_t*>(P.c) + at;
-          *c = bf16_bits(P.accumulate ? widen1(*c) + x : x);
-        }
-      }
-}
-
-// ------------------------------------------------- full tiles, straight to LDS
+// ---------------------------------------------------------------------- the tiles
 // BM x BN of C by WM x WN waves, k in steps of 64.  Both operands' tiles are copied
 // from global memory to LDS without passing registers, into one of two buffers while
 // the matrix cores work on the other; every wave reads the fragments of a quarter of a
@@ -220,52 +140,71 @@ struct Tile {
 };
 
 // Loader of one operand: where the lane's lines of a step lie, as a byte offset each
-// from an address that all lanes share.
-template <bool T, int R, int THREADS>
+// from an address that all lanes share.  DIRECT: copied to LDS without passing
+// registers, which takes 16-byte places, whole chunks and offsets of 32 bits; else read
+// from any address into registers, a step ahead, and stored.
+template <bool DIRECT, bool T, int R, int THREADS>
 struct Loader {
   typedef Tile<T, R, THREADS> L;
+  typedef u16x8 Chunk __attribute__((aligned(2)));
   const char* from;
-  int step_bytes;              // T only
-  uint32_t at[L::kLoads];
+  std::conditional_t<DIRECT, int, int64_t> step_bytes;   // T only
+  std::conditional_t<DIRECT, uint32_t, int64_t> at[L::kLoads];
+  int cols;                                              // !DIRECT, T: columns that exist from r0 on
+  u16x8 held[DIRECT ? 1 : L::kLoads];
 
   // Rows [r0, end) of the operand (lines, or columns where T); those behind read one
   // that exists, and what becomes of them is not stored.
   __device__ __forceinline__ void set(const uint16_t* base, int64_t stride, int r0, int end) {
-    if constexpr (T) step_bytes = uniform(2 * kStepK * int(stride));
+    typedef std::conditional_t<DIRECT, int, int64_t> Offset;
+    if constexpr (T) step_bytes = Offset(uniform(2 * kStepK * stride));
     from = reinterpret_cast<const char*>(uniform(int64_t(reinterpret_cast<uintptr_t>(base + (T ? r0 : r0 * stride)))));
-    const int left = end - r0, s = int(stride);
+    const Offset s = Offset(stride);
+    cols = end - r0;
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
       const int line = L::line(i), c = 8 * L::chunk(i);
-      at[i] = 2u * uint32_t(T ? line * s + (c < left ? c : 0) : std::min(line, left - 1) * s + c);
+      at[i] = 2 * (T ? line * s + (c < cols ? c : 0) : std::min(line, cols - 1) * s + c);
     }
   }
+  __device__ __forceinline__ u16x8 chunk(int i, int n) const {  // the first n of its elements
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(from + at[i]);
+    u16x8 x = {};
+    if (n >= 8) {
+      x = *reinterpret_cast<const Chunk*>(p);
+    } else {
+      for (int e = 0; e < n; ++e) x[e] = p[e];
+    }
+    return x;
+  }
+  // of a line of T, whose chunk of columns may be cut off (not where chunks are whole)
+  __device__ __forceinline__ int columns(int i) const { return DIRECT || !T ? 8 : cols - 8 * L::chunk(i); }
+
   __device__ __forceinline__ void copy(uint16_t* lds, int wave) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know the descriptor's type
     const auto all = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, -1, 0x00020000);
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(all, (GRO_LDS void*)(lds + wave * 512 + i * THREADS * 8), 16, at[i], 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(all, (GRO_LDS void*)(lds + wave * 512 + i * THREADS * 8), 16, int(at[i]), 0, 0, 0);
 #endif
-    from += T ? step_bytes : 2 * kStepK;
+    advance();
   }
-  // A step of `left` < 64 k: zeros behind them.
+  __device__ __forceinline__ void advance() { from += T ? step_bytes : 2 * kStepK; }
+  __device__ __forceinline__ void fetch() {
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) held[i] = chunk(i, columns(i));
+    advance();
+  }
+  __device__ __forceinline__ void store(uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < L::kLoads; ++i) *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = held[i];
+  }
+  // A step of `left` < kStepK k: zeros behind them.
   __device__ __forceinline__ void copy_part(uint16_t* lds, int left) const {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
-      u16x8 x = {};
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(from + at[i]);
-      if constexpr (T) {
-        if (L::line(i) < left) x = *reinterpret_cast<const u16x8*>(p);
-      } else {
-        const int n = left - 8 * L::chunk(i);
-        if (n >= 8) {
-          x = *reinterpret_cast<const u16x8*>(p);
-        } else {
-          for (int e = 0; e < n; ++e) x[e] = p[e];
-        }
-      }
-      *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = x;
+      const int n = T ? (L::line(i) < left ? columns(i) : 0) : left - 8 * L::chunk(i);
+      *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = chunk(i, n);
     }
   }
 };
@@ -310,6 +249,11 @@ __device__ __forceinline__ void step_barrier() {
   // the builtin for LDS, so that the compiler knows and adds no waits of its own behind it
   __builtin_amdgcn_s_waitcnt(0xc07f);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("s_barrier" ::: "memory");
 }
 
 // N neighbours of a row of C, of which `left` exist: four FP32 or eight BF16, 16 bytes.
@@ -373,7 +317,7 @@ struct Job {
   int expert, m0, m_end, n0, k_lo, k_n;
 };
 
-template <int MODE, int BM, int BN, int WM, int WN, bool CF>
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, bool CF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const ExpertsLaunch P) {
   constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
@@ -439,8 +383,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
   };
 
   constexpr int kWide = CF ? 4 : 8, kLanes = 32 / kWide, kRows = 64 / kLanes;
-  Loader<AT, BM, kThreads> la;
-  Loader<BT, BN, kThreads> lb;
+  Loader<DIRECT, AT, BM, kThreads> la;
+  Loader<DIRECT, BT, BN, kThreads> lb;
   constexpr int kLoads = decltype(la)::L::kLoads + decltype(lb)::L::kLoads, kStores = FM * FN * 32 / kRows;
   static_assert((kStages - 1) * kLoads + kStores < 64, "vmcnt counts to 63");
   Reader<AT, BM, FM> ra;
@@ -453,12 +397,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     la.copy(as[stage], wave);
     lb.copy(bs[stage], wave);
   };
+  const auto fetch = [&] {
+    la.fetch();
+    lb.fetch();
+  };
+  const auto store = [&](int stage) {
+    la.store(as[stage]);
+    lb.store(bs[stage]);
+  };
   const auto begin = [&](const Job& job) {
     la.set(P.a + (AT ? job.k_lo * P.a_stride : 0), P.a_stride, job.m0, job.m_end);
     lb.set(P.b + (MODE == kWeightGrad ? job.k_lo * P.b_stride : job.expert * P.expert_stride), P.b_stride, job.n0, n_end);
 #pragma unroll
     for (int t = 0; t < kStages; ++t)
-      if (job.k_n >= (t + 1) * kStepK) load(t);
+      if (job.k_n >= (t + 1) * kStepK) {
+        if constexpr (DIRECT) {
+          load(t);
+        } else {
+          fetch();
+          if (t < kStages - 1) store(t);
+        }
+      }
   };
 
   Job job;
@@ -487,22 +446,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     // step s has been loaded kStages - 1 steps ago; behind its loads are those of two more
     const auto step = [&](int s, auto number) {
       constexpr int kStage = decltype(number)::value;
+      if constexpr (!DIRECT) {
+        // step s + 3's, fetched a step ago, where step s - 1's were
+        if (s + kStages - 1 < steps) store((kStage + kStages - 1) % kStages);
+        if (s + kStages < steps) fetch();
+      }
       read(kStage, 1);
       multiply(0);
       interleave<kReads, kPart>();
-      if (s + kStages <= steps) {
+      if constexpr (!DIRECT) {
+        lds_barrier();
+      } else if (s + kStages <= steps) {
         if (stored && s < kStages - 1) step_barrier<(kStages - 2) * kLoads + kStores>();
         else step_barrier<(kStages - 2) * kLoads>();
       } else {
         step_barrier<0>();
       }
-      if (s + kStages < steps) load(kStage);
+      if (DIRECT && s + kStages < steps) load(kStage);
       read((kStage + 1) % kStages, 0);  // behind the last step, whatever the buffers hold
       multiply(1);
       interleave<kReads, kPart>();
     };
     if (steps > 0) {
-      if (steps >= kStages) {
+      if constexpr (!DIRECT) {
+        lds_barrier();
+      } else if (steps >= kStages) {
         if (stored) step_barrier<(kStages - 1) * kLoads + kStores>();
         else step_barrier<(kStages - 1) * kLoads>();
       } else {
@@ -592,35 +560,27 @@ bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
   return mode == kForward || (a.inner % 8 == 0 && (mode == kInputGrad || a.outer % 8 == 0));
 }
 
-template <int MODE, int BM, int BN, int WM, int WN>
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT>
 hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(BM, BN, WM * WN);
   const uint32_t n = xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
   const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
-  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, false>), grid, block, 0, s, a);
-  return hipGetLastError();
-}
-
-template <int MODE>
-hipError_t simple(const ExpertsLaunch& a, hipStream_t s) {
-  const dim3 grid(unsigned(tiles_of(a, ExpertsMode(MODE), kSimple, kSimple)));
-  if (a.c_fp32) hipLaunchKernelGGL((k_experts_simple<MODE, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_experts_simple<MODE, false>), grid, dim3(256), 0, s, a);
+  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
-  if (!direct(a, ExpertsMode(MODE))) return simple<MODE>(a, s);
+  if (!direct(a, ExpertsMode(MODE))) return tiles<MODE, 128, 128, 2, 2, false>(a, s);
   const int64_t n = MODE == kForward ? a.outer : a.inner, m = MODE == kWeightGrad ? a.outer : a.rows / a.n_experts;
-  if (m > 192 && n > 192) return tiles<MODE, 256, 256, 2, 4>(a, s);
-  return tiles<MODE, 128, 128, 2, 2>(a, s);
+  if (m > 192 && n > 192) return tiles<MODE, 256, 256, 2, 4, true>(a, s);
+  return tiles<MODE, 128, 128, 2, 2, true>(a, s);
 }
 
 }  // namespace
 
-int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode) { return tiles_of(a, mode, kSimple, kSimple); }
+int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode) { return tiles_of(a, mode, 128, 128); }
 
 int weight_grad_parts(int32_t, int64_t, int64_t, int64_t) { return 1; }
 
