@@ -11,6 +11,6 @@ from .binding import (  # noqa: F401
     gro_init_uniform, gro_reduce_norm, load,
     gro_clip_adamw_coded, gro_group_bind, gro_group_clip_adamw, gro_group_create, gro_group_destroy,
     gro_group_get_info, gro_group_get_norm, gro_group_norm, gro_moments_decode, gro_moments_encode,
-    gro_experts_forward, gro_experts_input_grad, gro_experts_weight_grad, gro_experts_weight_grad_workspace, gro_lookup,
+    gro_experts_forward, gro_experts_input_grad, gro_experts_weight_grad, gro_experts_workspace, gro_lookup,
     gro_lookup_grad, gro_lookup_grad_workspace, gro_row_sort, gro_row_sort_workspace,
 )

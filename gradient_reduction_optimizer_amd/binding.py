@@ -47,8 +47,8 @@ EXPORTS = ("gro_plan_create", "gro_plan_destroy", "gro_plan_get_info", "gro_plan
            "gro_clip_adamw_coded", "gro_moments_encode", "gro_moments_decode", "gro_group_create",
            "gro_group_destroy", "gro_group_get_info", "gro_group_bind", "gro_group_norm", "gro_group_clip_adamw",
            "gro_group_get_norm", "gro_row_sort_workspace", "gro_row_sort", "gro_lookup", "gro_lookup_grad_workspace",
-           "gro_lookup_grad", "gro_experts_forward", "gro_experts_input_grad", "gro_experts_weight_grad_workspace",
-           "gro_experts_weight_grad", "gro_last_error")
+           "gro_lookup_grad", "gro_experts_workspace", "gro_experts_forward", "gro_experts_input_grad", "gro_experts_weight_grad",
+           "gro_last_error")
 
 
 class gro_tensor_desc(ctypes.Structure):
@@ -179,9 +179,9 @@ def load() -> ctypes.CDLL:
     L.gro_lookup.argtypes = [M, I64, P, I32, D, M, P]
     L.gro_lookup_grad_workspace.argtypes = [I64, I64, ctypes.POINTER(U64)]
     L.gro_lookup_grad.argtypes = [M, P, P, D, I32, M, P, U64, P]
-    L.gro_experts_forward.argtypes = [M, W, P, M, P]
-    L.gro_experts_input_grad.argtypes = [M, W, P, M, P]
-    L.gro_experts_weight_grad_workspace.argtypes = [I32, I64, I64, I64, ctypes.POINTER(U64)]
+    L.gro_experts_workspace.argtypes = [I32, I64, I64, I64, ctypes.POINTER(U64)]
+    L.gro_experts_forward.argtypes = [M, W, P, M, P, U64, P]
+    L.gro_experts_input_grad.argtypes = [M, W, P, M, P, U64, P]
     L.gro_experts_weight_grad.argtypes = [M, M, P, I32, W, P, U64, P]
     L.gro_last_error.argtypes = []
     L.gro_last_error.restype = ctypes.c_char_p
@@ -479,18 +479,19 @@ def gro_lookup_grad(dy: gro_matrix, d_order: int, d_starts: int, scale: float, a
     _check(load().gro_lookup_grad(dy, d_order, d_starts, scale, accumulate, out, d_workspace, nbytes, stream))
 
 
-def gro_experts_forward(x: gro_matrix, weights: gro_experts, d_starts: int, y: gro_matrix, stream: int = 0) -> None:
+def gro_experts_workspace(n_experts: int, rows: int, inner: int, outer: int) -> int:
+    return _bytes(load().gro_experts_workspace, n_experts, rows, inner, outer)
+
+
+def gro_experts_forward(x: gro_matrix, weights: gro_experts, d_starts: int, y: gro_matrix, d_workspace: int = 0,
+                        nbytes: int = 0, stream: int = 0) -> None:
     """weights: ``gro_experts(data, outer, inner, stride, expert_stride, n_experts, type)``."""
-    _check(load().gro_experts_forward(x, weights, d_starts, y, stream))
+    _check(load().gro_experts_forward(x, weights, d_starts, y, d_workspace, nbytes, stream))
 
 
-def gro_experts_input_grad(dy: gro_matrix, weights: gro_experts, d_starts: int, dx: gro_matrix,
-                           stream: int = 0) -> None:
-    _check(load().gro_experts_input_grad(dy, weights, d_starts, dx, stream))
-
-
-def gro_experts_weight_grad_workspace(n_experts: int, rows: int, inner: int, outer: int) -> int:
-    return _bytes(load().gro_experts_weight_grad_workspace, n_experts, rows, inner, outer)
+def gro_experts_input_grad(dy: gro_matrix, weights: gro_experts, d_starts: int, dx: gro_matrix, d_workspace: int = 0,
+                           nbytes: int = 0, stream: int = 0) -> None:
+    _check(load().gro_experts_input_grad(dy, weights, d_starts, dx, d_workspace, nbytes, stream))
 
 
 def gro_experts_weight_grad(dy: gro_matrix, x: gro_matrix, d_starts: int, accumulate: bool, dw: gro_experts,

@@ -150,12 +150,14 @@ struct Loader {
   const char* from;
   std::conditional_t<DIRECT, int, int64_t> step_bytes;   // T only
   std::conditional_t<DIRECT, uint32_t, int64_t> at[L::kLoads];
-  int cols;                                              // !DIRECT, T: columns that exist from r0 on
+  int cols;                                              // T: columns that exist from r0 on
+  bool wide;                                             // a row has 8 elements at least
   u16x8 held[DIRECT ? 1 : L::kLoads];
 
   // Rows [r0, end) of the operand (lines, or columns where T); those behind read one
   // that exists, and what becomes of them is not stored.
-  __device__ __forceinline__ void set(const uint16_t* base, int64_t stride, int r0, int end) {
+  __device__ __forceinline__ void set(const uint16_t* base, int64_t stride, int r0, int end, int length) {
+    wide = length >= 8;
     typedef std::conditional_t<DIRECT, int, int64_t> Offset;
     if constexpr (T) step_bytes = Offset(uniform(2 * kStepK * stride));
     from = reinterpret_cast<const char*>(uniform(int64_t(reinterpret_cast<uintptr_t>(base + (T ? r0 : r0 * stride)))));
@@ -167,14 +169,23 @@ struct Loader {
       at[i] = 2 * (T ? line * s + (c < cols ? c : 0) : std::min(line, cols - 1) * s + c);
     }
   }
-  __device__ __forceinline__ u16x8 chunk(int i, int n) const {  // the first n of its elements
+  // The first n elements of a chunk, others being anything: where a row is cut off its
+  // last 8, for settle() to move to the front.
+  __device__ __forceinline__ u16x8 chunk(int i, int n) const {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(from + at[i]);
     u16x8 x = {};
-    if (n >= 8) {
-      x = *reinterpret_cast<const Chunk*>(p);
+    if (wide) {
+      if (n > 0) x = *reinterpret_cast<const Chunk*>(p - (n < 8 ? 8 - n : 0));
     } else {
-      for (int e = 0; e < n; ++e) x[e] = p[e];
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < n) x[e] = p[e];
     }
+    return x;
+  }
+  __device__ __forceinline__ u16x8 settle(u16x8 x, int n) const {
+    if (wide && n > 0 && n < 8)
+      x = __builtin_bit_cast(u16x8, __builtin_bit_cast(unsigned __int128, x) >> (16 * (8 - n)));
     return x;
   }
   // of a line of T, whose chunk of columns may be cut off (not where chunks are whole)
@@ -192,19 +203,22 @@ struct Loader {
   __device__ __forceinline__ void advance() { from += T ? step_bytes : 2 * kStepK; }
   __device__ __forceinline__ void fetch() {
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) held[i] = chunk(i, columns(i));
+    for (int i = 0; i < L::kLoads; ++i) {
+      if constexpr (T) held[i] = chunk(i, columns(i));
+      else held[i] = *reinterpret_cast<const Chunk*>(from + at[i]);  // 32 k are whole chunks
+    }
     advance();
   }
   __device__ __forceinline__ void store(uint16_t* lds) const {
 #pragma unroll
-    for (int i = 0; i < L::kLoads; ++i) *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = held[i];
+    for (int i = 0; i < L::kLoads; ++i) *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = settle(held[i], columns(i));
   }
   // A step of `left` < kStepK k: zeros behind them.
   __device__ __forceinline__ void copy_part(uint16_t* lds, int left) const {
 #pragma unroll
     for (int i = 0; i < L::kLoads; ++i) {
       const int n = T ? (L::line(i) < left ? columns(i) : 0) : left - 8 * L::chunk(i);
-      *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = chunk(i, n);
+      *reinterpret_cast<u16x8*>(lds + (threadIdx.x + i * THREADS) * 8) = settle(chunk(i, n), n);
     }
   }
 };
@@ -256,23 +270,25 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
-// N neighbours of a row of C, of which `left` exist: four FP32 or eight BF16, 16 bytes.
+// N neighbours of a row of C, of which `left` exist: four, or in BF16 eight too.
 template <bool CF, int N>
 __device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int left, const float (&x)[N]) {
   typedef f32x4 F4 __attribute__((aligned(4)));
-  typedef u16x8 B8 __attribute__((aligned(2)));
+  typedef uint16_t Bf16 __attribute__((ext_vector_type(N)));
+  typedef Bf16 Bf16Any __attribute__((aligned(2)));
   if (left >= N) {
     if constexpr (CF) {
+      static_assert(N == 4, "16 bytes");
       F4* c = reinterpret_cast<F4*>(static_cast<float*>(P.c) + at);
       f32x4 y = {x[0], x[1], x[2], x[3]};
       if (P.accumulate) y += *c;
       __builtin_nontemporal_store(y, c);
     } else {
-      B8* c = reinterpret_cast<B8*>(static_cast<uint16_t*>(P.c) + at);
-      u16x8 y = {};
+      Bf16Any* c = reinterpret_cast<Bf16Any*>(static_cast<uint16_t*>(P.c) + at);
+      Bf16 y = {};
       if (P.accumulate) y = *c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = bf16_bits(P.accumulate ? widen1(y[e]) + x[e] : x[e]);
+      for (int e = 0; e < N; ++e) y[e] = bf16_bits(P.accumulate ? widen1(y[e]) + x[e] : x[e]);
       __builtin_nontemporal_store(y, c);
     }
   } else {
@@ -314,10 +330,10 @@ __device__ __forceinline__ void in_wave_order() {
 
 // A tile of C: rows [m0, m_end) and columns from n0 on of an expert's, and the k it sums.
 struct Job {
-  int expert, m0, m_end, n0, k_lo, k_n;
+  int expert, m0, m_end, n0, k_lo, k_n, part;
 };
 
-template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, bool CF>
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, bool PARTS, bool CF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const ExpertsLaunch P) {
   constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
@@ -325,14 +341,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
   __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK], a1[BM * kStepK], a2[BM * kStepK], a3[BM * kStepK];
   __shared__ __attribute__((aligned(16))) uint16_t b0[BN * kStepK], b1[BN * kStepK], b2[BN * kStepK], b3[BN * kStepK];
   __shared__ __attribute__((aligned(16))) float results[WM * WN][32 * 32];
-  const int n_end = int(MODE == kForward ? P.outer : P.inner);
+  const int n_end = int(MODE == kForward ? P.outer : P.inner), k_size = int(MODE == kForward ? P.inner : P.outer);
+  const int m_size = int(P.outer);  // weight gradient only
   const uint32_t n_tiles = uint32_t((n_end + BN - 1) / BN);
   const int wave = uniform(int(threadIdx.x) >> 6), lane = int(threadIdx.x) & 63;
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
 
   const Tiles<BM> tiles(P);
   const uint32_t m_tiles = MODE == kWeightGrad ? uint32_t((P.outer + BM - 1) / BM) : tiles.total;
-  const uint32_t total = m_tiles * n_tiles * (MODE == kWeightGrad ? uint32_t(P.n_experts) : 1u);
+  const uint32_t whole = m_tiles * n_tiles * (MODE == kWeightGrad ? uint32_t(P.n_experts) : 1u);
+  const uint32_t total = PARTS ? whole * uint32_t(P.n_parts) : whole;
   // weight gradients: experts with more rows first, of the first 64
   int rank = 0;
   if constexpr (MODE == kWeightGrad) {
@@ -352,21 +370,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     const uint32_t round = b / kGrid, in_round = b % kGrid;
     const uint32_t i = xcd_order(turn && (round & 1) ? round * kGrid + (kGrid - 1 - in_round) : b, total, kChunk);
     if (i >= total) return false;
+    const uint32_t part = PARTS ? i / whole : 0, tile = i - part * whole;
     if constexpr (MODE == kWeightGrad) {
-      const Place p = banded(i % (m_tiles * n_tiles), m_tiles, n_tiles);
-      job.expert = by_length(int(i / (m_tiles * n_tiles)));
+      const Place p = banded(tile % (m_tiles * n_tiles), m_tiles, n_tiles);
+      job.expert = by_length(int(tile / (m_tiles * n_tiles)));
       const Run r = run_of(P, job.expert);
       job.m0 = int(p.m) * BM;
       job.n0 = int(p.n) * BN;
-      job.m_end = int(P.outer);
+      job.m_end = m_size;
       job.k_lo = uniform(r.lo);
       job.k_n = uniform(r.hi - r.lo);
     } else {
-      const Place p = banded(i, m_tiles, n_tiles);
+      const Place p = banded(tile, m_tiles, n_tiles);
       tiles.find(P, p.m, job.expert, job.m0, job.m_end);
       job.n0 = int(p.n) * BN;
       job.k_lo = 0;
-      job.k_n = int(MODE == kForward ? P.inner : P.outer);
+      job.k_n = k_size;
+    }
+    if constexpr (PARTS) {
+      job.part = int(part);
+      // a part of the steps, the last part with what is left behind whole ones
+      const int steps = job.k_n / kStepK, from = int(int64_t(steps) * part / P.n_parts) * kStepK;
+      const int to = job.part + 1 == P.n_parts ? job.k_n : int(int64_t(steps) * (part + 1) / P.n_parts) * kStepK;
+      job.k_lo += from;
+      job.k_n = to - from;
     }
     return true;
   };
@@ -406,8 +433,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     lb.store(bs[stage]);
   };
   const auto begin = [&](const Job& job) {
-    la.set(P.a + (AT ? job.k_lo * P.a_stride : 0), P.a_stride, job.m0, job.m_end);
-    lb.set(P.b + (MODE == kWeightGrad ? job.k_lo * P.b_stride : job.expert * P.expert_stride), P.b_stride, job.n0, n_end);
+    la.set(P.a + (AT ? job.k_lo * P.a_stride : job.k_lo), P.a_stride, job.m0, job.m_end, AT ? m_size : k_size);
+    lb.set(P.b + (BT ? job.k_lo * P.b_stride : job.k_lo) + (MODE == kWeightGrad ? 0 : job.expert * P.b_expert), P.b_stride, job.n0,
+           n_end, BT ? n_end : k_size);
 #pragma unroll
     for (int t = 0; t < kStages; ++t)
       if (job.k_n >= (t + 1) * kStepK) {
@@ -511,7 +539,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
       stored = false;
       continue;
     }
-    const int64_t base = MODE == kWeightGrad ? done.expert * P.expert_stride : 0;
+    const int64_t base = (MODE == kWeightGrad ? done.expert * P.c_expert : 0) + (PARTS ? done.part * P.c_part : 0);
     float* block = results[wave];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -542,6 +570,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
   }
 }
 
+// The parts' sums, added up in their order, to C: a workgroup has kJoinRows rows of a
+// tile, each lane its neighbours of one of them.
+constexpr int kJoinRows = 8;
+template <int MODE, int BM, int BN, bool CF>
+__global__ __launch_bounds__(kJoinRows * BN / 4) void k_experts_join(const ExpertsLaunch P) {
+  const int n_end = int(MODE == kForward ? P.outer : P.inner);
+  const uint32_t n_tiles = uint32_t((n_end + BN - 1) / BN);
+  const uint32_t block = blockIdx.x / (BM / kJoinRows), tile = block / n_tiles;
+  const int n0 = int(block % n_tiles) * BN;
+  int expert, m0, m_end;
+  if constexpr (MODE == kWeightGrad) {
+    const uint32_t m_tiles = uint32_t((P.outer + BM - 1) / BM);
+    expert = int(tile / m_tiles);
+    m0 = int(tile % m_tiles) * BM;
+    m_end = int(P.outer);
+    const Run r = run_of(P, expert);
+    if (P.accumulate && r.lo == r.hi) return;
+  } else {
+    const Tiles<BM> tiles(P);
+    if (tile >= tiles.total) return;
+    tiles.find(P, tile, expert, m0, m_end);
+  }
+  constexpr int kLanes = BN / 4;
+  typedef f32x4 F4 __attribute__((aligned(4)));
+  const int n = n0 + int(threadIdx.x) % kLanes * 4, left = n_end - n;
+  const int m = m0 + int(blockIdx.x % (BM / kJoinRows)) * kJoinRows + int(threadIdx.x) / kLanes;
+  if (left <= 0 || m >= m_end) return;
+  const float* p = P.partials + (MODE == kWeightGrad ? int64_t(expert) * P.outer * P.inner : 0) + int64_t(m) * n_end + n;
+  float x[4] = {};
+#pragma unroll 8
+  for (int part = 0; part < P.n_parts; ++part, p += P.c_part) {
+    f32x4 y = {};
+    if (left >= 4) {
+      y = *reinterpret_cast<const F4*>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (e < left) y[e] = p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += y[e];
+  }
+  store_c<CF, 4>(P, (MODE == kWeightGrad ? expert * P.c_expert : 0) + m * P.c_stride + n, left, x);
+}
+
 // Tiles of BM x BN that cover C: every expert's last one may be a part of one.
 int64_t tiles_of(const ExpertsLaunch& a, ExpertsMode mode, int64_t bm, int64_t bn) {
   const int64_t n = mode == kForward ? a.outer : a.inner, across = (n + bn - 1) / bn;
@@ -555,7 +628,7 @@ bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
   const auto fits = [](const void* p, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && stride < (int64_t(1) << 22);
   };
-  if (!fits(a.a, a.a_stride) || !fits(a.b, a.b_stride) || a.expert_stride % 8 != 0) return false;
+  if (!fits(a.a, a.a_stride) || !fits(a.b, a.b_stride) || a.b_expert % 8 != 0) return false;
   // an operand whose rows of C lie innermost is copied 8 of them at a time
   return mode == kForward || (a.inner % 8 == 0 && (mode == kInputGrad || a.outer % 8 == 0));
 }
@@ -565,14 +638,36 @@ hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(BM, BN, WM * WN);
   const uint32_t n = xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
   const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
-  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false>), grid, block, 0, s, a);
+  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+// 128 x 128 tiles in parts of their k, and the join of those.
+template <int MODE, bool DIRECT>
+hipError_t in_parts(const ExpertsLaunch& a, hipStream_t s) {
+  ExpertsLaunch b = a;
+  b.c = a.partials;
+  b.c_fp32 = 1;
+  b.accumulate = 0;
+  b.c_stride = MODE == kForward ? a.outer : a.inner;
+  b.c_expert = a.outer * a.inner;
+  constexpr uint32_t units = tile_units(128, 128, 4);
+  const uint32_t n = uint32_t(tiles_of(a, ExpertsMode(MODE), 128, 128));
+  const dim3 places(std::min(xcd_numbers(n * uint32_t(a.n_parts), 32 * units), 256 * units)), grid(n * (128 / kJoinRows));
+  hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, true, true>), places, dim3(256), 0, s, b);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (a.c_fp32) hipLaunchKernelGGL((k_experts_join<MODE, 128, 128, true>), grid, dim3(kJoinRows * 32), 0, s, a);
+  else hipLaunchKernelGGL((k_experts_join<MODE, 128, 128, false>), grid, dim3(kJoinRows * 32), 0, s, a);
   return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
-  if (!direct(a, ExpertsMode(MODE))) return tiles<MODE, 128, 128, 2, 2, false>(a, s);
+  const bool whole = direct(a, ExpertsMode(MODE));
+  if (a.n_parts > 1) return whole ? in_parts<MODE, true>(a, s) : in_parts<MODE, false>(a, s);
+  if (!whole) return tiles<MODE, 128, 128, 2, 2, false>(a, s);
   const int64_t n = MODE == kForward ? a.outer : a.inner, m = MODE == kWeightGrad ? a.outer : a.rows / a.n_experts;
   if (m > 192 && n > 192) return tiles<MODE, 256, 256, 2, 4, true>(a, s);
   return tiles<MODE, 128, 128, 2, 2, true>(a, s);
@@ -582,7 +677,19 @@ hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
 
 int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode) { return tiles_of(a, mode, 128, 128); }
 
-int weight_grad_parts(int32_t, int64_t, int64_t, int64_t) { return 1; }
+// Parts that the sums over k are cut into where there are few tiles for the GPU's 512
+// places of 128 x 128: each of 8 steps or more.
+int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inner, int64_t outer) {
+  if (n_experts <= 0 || rows <= 0 || inner <= 0 || outer <= 0) return 1;
+  ExpertsLaunch a = {};
+  a.n_experts = n_experts;
+  a.rows = rows;
+  a.inner = inner;
+  a.outer = outer;
+  const int64_t k = mode == kForward ? inner : mode == kInputGrad ? outer : rows / n_experts;
+  const int64_t parts = std::min(512 / tiles_of(a, mode, 128, 128), k / (8 * kStepK));
+  return int(std::min<int64_t>(std::max<int64_t>(parts, 1), 32));
+}
 
 hipError_t launch_experts(const ExpertsLaunch& a, ExpertsMode mode, hipStream_t s) {
   const bool nothing = mode == kForward ? a.outer <= 0 : mode == kInputGrad ? a.inner <= 0 : a.inner <= 0 || a.outer <= 0;

@@ -98,20 +98,22 @@ struct ExpertsLaunch {
   const uint16_t* b;        // forward and input gradient W, weight gradient x
   void* c;                  // y, dx, dW
   int64_t a_stride, b_stride, c_stride;
-  int64_t expert_stride;    // of the weights
+  int64_t b_expert;         // from one expert's matrix to the next: of the weights ...
+  int64_t c_expert;         // ... or of their gradients
   const int32_t* starts;
   int32_t n_experts;
   int64_t rows;             // rows that starts may name
   int64_t inner, outer;
   int32_t c_fp32;
   int32_t accumulate;       // weight gradient only
-  float* partials;          // weight gradient in several parts of the rows
-  int32_t n_parts;
+  int32_t n_parts;          // of the sums over k; more than one:
+  float* partials;          // [n_parts][C without gaps]
+  int64_t c_part;           // elements of one part
 };
 // The most workgroups that a call launches (a launch has fewer than 2^32 lanes).
 int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode);
 constexpr int64_t kMaxExpertsTiles = (int64_t(1) << 23) - 1;
-int weight_grad_parts(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer);
+int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inner, int64_t outer);
 hipError_t launch_experts(const ExpertsLaunch& a, ExpertsMode mode, hipStream_t s);
 
 }  // namespace gro

@@ -159,9 +159,12 @@ int check_bf16(int32_t type, const char* what) {
   return GRO_OK;
 }
 
+// FP32 sums of a product in parts.
+uint64_t parts_workspace(int parts, int64_t elems) { return parts > 1 ? up256(uint64_t(parts) * uint64_t(elems) * 4) : 0; }
+
 // Forward (mode kForward: from inner to outer) and input gradient (the other way).
-int run_product(const gro_matrix* in, const gro_experts* w, const int32_t* starts, const gro_matrix* out,
-                ExpertsMode mode, const char* in_name, const char* out_name, void* stream) {
+int run_product(const gro_matrix* in, const gro_experts* w, const int32_t* starts, const gro_matrix* out, void* d_workspace,
+                uint64_t bytes, ExpertsMode mode, const char* in_name, const char* out_name, void* stream) {
   clear_error();
   int rc = check_matrix(in, in_name);
   if (rc == GRO_OK) rc = check_weights(w, "weights");
@@ -175,9 +178,18 @@ int run_product(const gro_matrix* in, const gro_experts* w, const int32_t* start
     return set_error(GRO_E_INVALID, "%s is %lld x %lld and %s %lld x %lld with weights of %lld x %lld", in_name,
                      (long long)in->rows, (long long)in->cols, out_name, (long long)out->rows, (long long)out->cols,
                      (long long)w->outer, (long long)w->inner);
-  rc = check_apart(area_of(*out), out_name, area_of(*in), in_name);
+  const int parts = experts_parts(mode, w->n_experts, in->rows, w->inner, w->outer);
+  const uint64_t need = parts_workspace(parts, in->rows * to);
+  rc = check_workspace(d_workspace, bytes, need);
+  const Area ws = area_of(d_workspace, need);
+  if (rc == GRO_OK) rc = check_apart(area_of(*out), out_name, area_of(*in), in_name);
   if (rc == GRO_OK) rc = check_apart(area_of(*out), out_name, area_of(*w), "the weights");
-  if (rc == GRO_OK) rc = check_apart(area_of(*out), out_name, area_of(starts, uint64_t(w->n_experts + 1) * 4), "d_starts");
+  const Area runs = area_of(starts, uint64_t(w->n_experts + 1) * 4);
+  if (rc == GRO_OK) rc = check_apart(area_of(*out), out_name, runs, "d_starts");
+  if (rc == GRO_OK) rc = check_apart(ws, "the workspace", area_of(*out), out_name);
+  if (rc == GRO_OK) rc = check_apart(ws, "the workspace", area_of(*in), in_name);
+  if (rc == GRO_OK) rc = check_apart(ws, "the workspace", area_of(*w), "the weights");
+  if (rc == GRO_OK) rc = check_apart(ws, "the workspace", runs, "d_starts");
   if (rc != GRO_OK) return rc;
   ExpertsLaunch a = {};
   a.a = static_cast<const uint16_t*>(in->data);
@@ -186,21 +198,19 @@ int run_product(const gro_matrix* in, const gro_experts* w, const int32_t* start
   a.a_stride = in->stride;
   a.b_stride = w->stride;
   a.c_stride = out->stride;
-  a.expert_stride = w->expert_stride;
+  a.b_expert = w->expert_stride;
   a.starts = starts;
   a.n_experts = w->n_experts;
   a.rows = in->rows;
   a.inner = w->inner;
   a.outer = w->outer;
   a.c_fp32 = out->type == GRO_FP32;
+  a.n_parts = parts;
+  a.partials = static_cast<float*>(d_workspace);
+  a.c_part = in->rows * to;
   if (experts_tiles(a, mode) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product too large for one launch");
   const hipError_t e = launch_experts(a, mode, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GRO_OK : hip_fail(e, "experts' product launch");
-}
-
-uint64_t weight_grad_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer) {
-  const int parts = weight_grad_parts(n_experts, rows, inner, outer);
-  return parts > 1 ? up256(uint64_t(parts) * uint64_t(n_experts) * uint64_t(inner) * uint64_t(outer) * 4) : 0;
 }
 
 }  // namespace
@@ -329,26 +339,31 @@ extern "C" int gro_lookup_grad(const gro_matrix* dy, const int32_t* d_order, con
   return e == hipSuccess ? GRO_OK : hip_fail(e, "lookup gradient launch");
 }
 
-extern "C" int gro_experts_forward(const gro_matrix* x, const gro_experts* weights, const int32_t* d_starts,
-                                   const gro_matrix* y, void* stream) {
-  return run_product(x, weights, d_starts, y, kForward, "x", "y", stream);
-}
-
-extern "C" int gro_experts_input_grad(const gro_matrix* dy, const gro_experts* weights, const int32_t* d_starts,
-                                      const gro_matrix* dx, void* stream) {
-  return run_product(dy, weights, d_starts, dx, kInputGrad, "dy", "dx", stream);
-}
-
-extern "C" int gro_experts_weight_grad_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer,
-                                                 uint64_t* bytes) {
+extern "C" int gro_experts_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer, uint64_t* bytes) {
   clear_error();
   const int rc = check_sizes(rows, inner, bytes, "columns");
   if (rc != GRO_OK) return rc;
   if (n_experts < 0 || n_experts > GRO_MAX_EXPERTS || outer < 0 || outer > kMaxIds ||
-      double(n_experts) * double(inner) * double(outer) > double(kMaxElems))
-    return set_error(GRO_E_INVALID, "%d experts of %lld x %lld", n_experts, (long long)outer, (long long)inner);
-  *bytes = weight_grad_workspace(n_experts, rows, inner, outer);
+      double(n_experts) * double(inner) * double(outer) > double(kMaxElems) ||
+      double(rows) * double(std::max(inner, outer)) > double(kMaxElems))
+    return set_error(GRO_E_INVALID, "%d experts of %lld x %lld, %lld rows", n_experts, (long long)outer, (long long)inner,
+                     (long long)rows);
+  const auto need = [&](ExpertsMode mode, int64_t elems) {
+    return parts_workspace(experts_parts(mode, n_experts, rows, inner, outer), elems);
+  };
+  *bytes = std::max(std::max(need(kForward, rows * outer), need(kInputGrad, rows * inner)),
+                    need(kWeightGrad, n_experts * outer * inner));
   return GRO_OK;
+}
+
+extern "C" int gro_experts_forward(const gro_matrix* x, const gro_experts* weights, const int32_t* d_starts,
+                                   const gro_matrix* y, void* d_workspace, uint64_t bytes, void* stream) {
+  return run_product(x, weights, d_starts, y, d_workspace, bytes, kForward, "x", "y", stream);
+}
+
+extern "C" int gro_experts_input_grad(const gro_matrix* dy, const gro_experts* weights, const int32_t* d_starts,
+                                      const gro_matrix* dx, void* d_workspace, uint64_t bytes, void* stream) {
+  return run_product(dy, weights, d_starts, dx, d_workspace, bytes, kInputGrad, "dy", "dx", stream);
 }
 
 extern "C" int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x, const int32_t* d_starts,
@@ -367,7 +382,9 @@ extern "C" int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x
                      (long long)dy->rows, (long long)dy->cols, (long long)x->rows, (long long)x->cols,
                      (long long)dw->outer, (long long)dw->inner);
   if (accumulate != 0 && accumulate != 1) return set_error(GRO_E_INVALID, "accumulate is 0 or 1");
-  const uint64_t need = weight_grad_workspace(dw->n_experts, dy->rows, dw->inner, dw->outer);
+  const int parts = experts_parts(kWeightGrad, dw->n_experts, dy->rows, dw->inner, dw->outer);
+  const int64_t elems = dw->n_experts * dw->outer * dw->inner;
+  const uint64_t need = parts_workspace(parts, elems);
   rc = check_workspace(d_workspace, bytes, need);
   if (rc != GRO_OK) return rc;
   const Area o = area_of(*dw), ws = area_of(d_workspace, need),
@@ -387,7 +404,7 @@ extern "C" int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x
   a.a_stride = dy->stride;
   a.b_stride = x->stride;
   a.c_stride = dw->stride;
-  a.expert_stride = dw->expert_stride;
+  a.c_expert = dw->expert_stride;
   a.starts = d_starts;
   a.n_experts = dw->n_experts;
   a.rows = dy->rows;
@@ -396,7 +413,8 @@ extern "C" int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x
   a.c_fp32 = dw->type == GRO_FP32;
   a.accumulate = accumulate;
   a.partials = static_cast<float*>(d_workspace);
-  a.n_parts = weight_grad_parts(dw->n_experts, dy->rows, dw->inner, dw->outer);
+  a.n_parts = parts;
+  a.c_part = elems;
   if (experts_tiles(a, kWeightGrad) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product too large for one launch");
   const hipError_t e = launch_experts(a, kWeightGrad, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GRO_OK : hip_fail(e, "experts' weight gradient launch");

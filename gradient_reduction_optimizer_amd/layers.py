@@ -196,7 +196,10 @@ def _product(fn, in_name, rows, weight, starts, out, out_name, cols, dtype, stre
     if not given:  # rows that no expert has are not written by the product
         out = torch.zeros((rows.shape[0], getattr(w, cols)), dtype=dtype or rows.dtype, device=device)
     x, y = _matrix(in_name, rows, device, _BF16), _matrix(out_name, out, device)
-    _call(device, stream, (rows, weight, starts, out), not given, fn, x, w, starts.data_ptr(), y)
+    nbytes = B.gro_experts_workspace(w.n_experts, x.rows, w.inner, w.outer)
+    room = _room(nbytes, device)
+    _call(device, stream, (rows, weight, starts, out, room), not given or room is not None, fn, x, w, starts.data_ptr(), y,
+          _aligned(room) if nbytes else 0, nbytes)
     if given:
         _wrote(out)
     return out
@@ -228,7 +231,7 @@ def experts_weight_grad(dy, x, starts, out=None, accumulate: bool = False, dtype
         out = torch.empty((max(starts.numel() - 1, 0), d.cols, r.cols), dtype=dtype or dy.dtype, device=device)
     w = _experts("out", out, device)
     _index("starts", starts, device, _I32, w.n_experts + 1)
-    nbytes = B.gro_experts_weight_grad_workspace(w.n_experts, d.rows, w.inner, w.outer)
+    nbytes = B.gro_experts_workspace(w.n_experts, d.rows, w.inner, w.outer)
     room = _room(nbytes, device)
     _call(device, stream, (dy, x, starts, out, room), not given or room is not None, B.gro_experts_weight_grad, d, r,
           starts.data_ptr(), bool(accumulate), w, _aligned(room) if nbytes else 0, nbytes)

@@ -566,13 +566,15 @@ typedef struct gro_experts {
  * x, dy and W are BF16, results BF16 or FP32; products are summed in FP32 and rounded
  * once.  Rows in front of d_starts[0] and from d_starts[n_experts] on are neither
  * read nor written.  An expert's result depends on its own rows alone: infinities and
- * NaN of other rows do not reach it. */
+ * NaN of other rows do not reach it.  Few rows or small matrices leave few tiles for
+ * the GPU; their sums are then taken in parts, whose workspace (256-byte aligned) has
+ * the bytes that gro_experts_workspace gives, enough for any of the three and 0 for
+ * most sizes. */
+int gro_experts_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer, uint64_t* bytes);
 int gro_experts_forward(const gro_matrix* x, const gro_experts* weights, const int32_t* d_starts,
-                        const gro_matrix* y, void* stream);
+                        const gro_matrix* y, void* d_workspace, uint64_t bytes, void* stream);
 int gro_experts_input_grad(const gro_matrix* dy, const gro_experts* weights, const int32_t* d_starts,
-                           const gro_matrix* dx, void* stream);
-int gro_experts_weight_grad_workspace(int32_t n_experts, int64_t rows, int64_t inner, int64_t outer,
-                                      uint64_t* bytes);
+                           const gro_matrix* dx, void* d_workspace, uint64_t bytes, void* stream);
 int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x, const int32_t* d_starts,
                             int32_t accumulate, const gro_experts* dw, void* d_workspace, uint64_t bytes,
                             void* stream);

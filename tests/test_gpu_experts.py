@@ -45,6 +45,11 @@ CASES = {
     "no outer": ([4, 2], 0, 1, 24, 0),
     "thin": ([100, 30], 0, 0, 1, 1),
     "many experts": ([(7 * i) % 5 for i in range(200)], 3, 3, 64, 40),
+    "few rows, long sums": ([3, 0, 17], 1, 1, 2056, 1320),
+    "few odd rows, long sums": ([5, 2], 0, 3, 1031, 519),
+    "one wide row": ([1], 0, 0, 4101, 24),
+    "long and thin": ([2500, 0, 9], 0, 0, 45, 72),
+    "long and narrow": ([0, 3333], 2, 0, 5, 6),
     "batch": ([300, 500, 0, 800, 250], 0, 50, 512, 1024),
 }
 LAYOUTS = [(0, 0), (8, 0), (64, 8), (3, 1), (0, 5)]

@@ -85,7 +85,7 @@ def test_products_refuse():
 
     def call(fn, base, **k):
         a = {**base, **k}
-        fn(a["rows"], a["w"], a["starts"], a["out"], 0)
+        fn(a["rows"], a["w"], a["starts"], a["out"], a.get("ws", 0), a.get("bytes", 0), 0)
 
     shared = (dict(w=W(0, 4, 16, 8)), dict(w=W(BB + 1, 4, 16, 8)), dict(w=W(BB, 4, 16, 8, 7)), dict(w=W(BB, 4, 16, 8, expert=127)),
               dict(w=W(BB, -1, 16, 8)), dict(w=W(BB, B.GRO_MAX_EXPERTS + 1, 16, 8)), dict(w=W(BB, 4, 16, 8, type=FP32)),
@@ -97,6 +97,13 @@ def test_products_refuse():
         refused(lambda bad=bad: call(B.gro_experts_forward, ok, **bad))
     for bad in (*shared, dict(rows=M(A, 100, 16, type=FP32)), dict(rows=M(A, 100, 8)), dict(out=M(D, 100, 16))):
         refused(lambda bad=bad: call(B.gro_experts_input_grad, back, **bad))
+    # few tiles and a long sum, which is taken in parts
+    need = B.gro_experts_workspace(1, 20, 8192, 64)
+    long = dict(rows=M(A, 20, 8192), w=W(BB, 1, 64, 8192), out=M(D, 20, 64), ws=WS, bytes=need)
+    assert need >= 2 * 20 * 64 * 4
+    for bad in (dict(ws=0), dict(ws=WS + 8), dict(bytes=need - 1 if need == 32 * 20 * 64 * 4 else 0), dict(ws=A), dict(ws=BB),
+                dict(ws=C - 256), dict(ws=D)):
+        refused(lambda bad=bad: call(B.gro_experts_forward, ok, **{**long, **bad}))
     huge = dict(rows=M(A, 2 ** 31 - 2 ** 17, 64), w=W(BB, 1, 2 ** 24, 64), out=M(1 << 50, 2 ** 31 - 2 ** 17, 2 ** 24))
     refused(lambda: call(B.gro_experts_forward, ok, **huge))
 
@@ -114,7 +121,8 @@ def test_weight_gradient_refuses():
                 dict(dw=W(D, 4, 16, 8, 4)), dict(dw=W(D, 4, 15, 8))):
         refused(lambda bad=bad: grad(**bad))
     # long runs and few tiles are summed in parts
-    need = B.gro_experts_weight_grad_workspace(1, 1 << 20, 64, 64)
+    need = B.gro_experts_workspace(1, 1 << 20, 64, 64)
+    assert need > 0
     if need:
         long = dict(dy=M(A, 1 << 20, 64), x=M(BB, 1 << 20, 64), dw=W(D, 1, 64, 64), bytes=need)
         for bad in (dict(ws=0), dict(ws=WS + 8), dict(bytes=need - 1), dict(ws=A), dict(ws=BB), dict(ws=C - 256), dict(ws=D)):
@@ -124,7 +132,7 @@ def test_weight_gradient_refuses():
 def test_workspaces():
     for fn, bad in ((B.gro_row_sort_workspace, ((-1, 5), (5, -1), (2 ** 31, 5), (5, B.GRO_MAX_TABLE_ROWS + 1))),
                     (B.gro_lookup_grad_workspace, ((-1, 5), (5, -1), (2 ** 31, 5))),
-                    (B.gro_experts_weight_grad_workspace, ((-1, 5, 5, 5), (5000, 5, 5, 5), (5, -1, 5, 5), (5, 5, -1, 5),
+                    (B.gro_experts_workspace, ((-1, 5, 5, 5), (5000, 5, 5, 5), (5, -1, 5, 5), (5, 5, -1, 5),
                                                            (5, 5, 5, -1), (4096, 5, 2 ** 20, 2 ** 20)))):
         for args in bad:
             refused(fn, *args)
@@ -204,7 +212,7 @@ def test_python_calls_hand_over_what_the_tensors_are(on_gpu):
     x, y = bf(5, 24)[:, 8:16], bf(5, 20)[:, :16]
     starts = torch.zeros(4, dtype=torch.int32)
     assert L.experts_forward(x, w, starts, out=y) is y
-    name, (mx, mw, s, my, stream) = on_gpu.pop()
+    name, (mx, mw, s, my, ws, nbytes, stream) = on_gpu.pop()
     assert name == "gro_experts_forward" and s == starts.data_ptr() and stream == 7
     assert (mx.data, mx.rows, mx.cols, mx.stride, mx.type) == (x.data_ptr(), 5, 8, 24, BF16)
     assert (mw.data, mw.outer, mw.inner, mw.stride, mw.expert_stride, mw.n_experts) == (w.data_ptr(), 16, 8, 32, 1280, 3)
