@@ -333,9 +333,21 @@ struct Job {
   int expert, m0, m_end, n0, k_lo, k_n, part;
 };
 
-template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, bool PARTS, bool CF>
+// What a launch covers: every tile; every tile in parts of its k; of 256 x 256 tiles
+// those that fill the GPU a whole number of times, where so few are left that they are
+// done sooner in quarters; those quarters.
+enum Cover { kAll, kParts, kRounds, kQuarters };
+// Tiles of `total` that are left to quarters.
+__device__ __forceinline__ uint32_t left_over(uint32_t total) {
+  const uint32_t n = total % 256;
+  return total > 256 && n <= 128 ? n : 0;
+}
+
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER, bool CF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const ExpertsLaunch P) {
   constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
+  constexpr bool PARTS = COVER == kParts, QUARTERS = COVER == kQuarters;
+  constexpr int TM = QUARTERS ? 2 * BM : BM, TN = QUARTERS ? 2 * BN : BN;  // as tiles are numbered
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
   constexpr uint32_t kChunk = 32 * tile_units(BM, BN, WM * WN), kGrid = 8 * kChunk;
   __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK], a1[BM * kStepK], a2[BM * kStepK], a3[BM * kStepK];
@@ -343,14 +355,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
   __shared__ __attribute__((aligned(16))) float results[WM * WN][32 * 32];
   const int n_end = int(MODE == kForward ? P.outer : P.inner), k_size = int(MODE == kForward ? P.inner : P.outer);
   const int m_size = int(P.outer);  // weight gradient only
-  const uint32_t n_tiles = uint32_t((n_end + BN - 1) / BN);
+  const uint32_t n_tiles = uint32_t((n_end + TN - 1) / TN);
   const int wave = uniform(int(threadIdx.x) >> 6), lane = int(threadIdx.x) & 63;
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
 
-  const Tiles<BM> tiles(P);
-  const uint32_t m_tiles = MODE == kWeightGrad ? uint32_t((P.outer + BM - 1) / BM) : tiles.total;
+  const Tiles<TM> tiles(P);
+  const uint32_t m_tiles = MODE == kWeightGrad ? uint32_t((P.outer + TM - 1) / TM) : tiles.total;
   const uint32_t whole = m_tiles * n_tiles * (MODE == kWeightGrad ? uint32_t(P.n_experts) : 1u);
-  const uint32_t total = PARTS ? whole * uint32_t(P.n_parts) : whole;
+  const uint32_t rest = COVER == kRounds || QUARTERS ? left_over(whole) : 0;
+  const uint32_t total = PARTS ? whole * uint32_t(P.n_parts) : QUARTERS ? 4 * rest : whole - rest;
   // weight gradients: experts with more rows first, of the first 64
   int rank = 0;
   if constexpr (MODE == kWeightGrad) {
@@ -370,7 +383,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     const uint32_t round = b / kGrid, in_round = b % kGrid;
     const uint32_t i = xcd_order(turn && (round & 1) ? round * kGrid + (kGrid - 1 - in_round) : b, total, kChunk);
     if (i >= total) return false;
-    const uint32_t part = PARTS ? i / whole : 0, tile = i - part * whole;
+    const uint32_t part = PARTS ? i / whole : 0, tile = QUARTERS ? whole - rest + i / 4 : i - part * whole;
     if constexpr (MODE == kWeightGrad) {
       const Place p = banded(tile % (m_tiles * n_tiles), m_tiles, n_tiles);
       job.expert = by_length(int(tile / (m_tiles * n_tiles)));
@@ -383,7 +396,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     } else {
       const Place p = banded(tile, m_tiles, n_tiles);
       tiles.find(P, p.m, job.expert, job.m0, job.m_end);
-      job.n0 = int(p.n) * BN;
+      job.n0 = int(p.n) * TN;
+      if constexpr (QUARTERS) {
+        job.m0 += int(i & 1) * BM;
+        job.n0 += int(i >> 1 & 1) * BN;
+        if (job.m0 >= job.m_end || job.n0 >= n_end) return false;
+      }
       job.k_lo = 0;
       job.k_n = k_size;
     }
@@ -633,13 +651,13 @@ bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
   return mode == kForward || (a.inner % 8 == 0 && (mode == kInputGrad || a.outer % 8 == 0));
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT>
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER = kAll>
 hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(BM, BN, WM * WN);
-  const uint32_t n = xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
+  const uint32_t n = COVER == kQuarters ? 256 * units : xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
   const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
-  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, false, false>), grid, block, 0, s, a);
+  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -655,7 +673,7 @@ hipError_t in_parts(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(128, 128, 4);
   const uint32_t n = uint32_t(tiles_of(a, ExpertsMode(MODE), 128, 128));
   const dim3 places(std::min(xcd_numbers(n * uint32_t(a.n_parts), 32 * units), 256 * units)), grid(n * (128 / kJoinRows));
-  hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, true, true>), places, dim3(256), 0, s, b);
+  hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, kParts, true>), places, dim3(256), 0, s, b);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.c_fp32) hipLaunchKernelGGL((k_experts_join<MODE, 128, 128, true>), grid, dim3(kJoinRows * 32), 0, s, a);
@@ -669,7 +687,17 @@ hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
   if (a.n_parts > 1) return whole ? in_parts<MODE, true>(a, s) : in_parts<MODE, false>(a, s);
   if (!whole) return tiles<MODE, 128, 128, 2, 2, false>(a, s);
   const int64_t n = MODE == kForward ? a.outer : a.inner, m = MODE == kWeightGrad ? a.outer : a.rows / a.n_experts;
-  if (m > 192 && n > 192) return tiles<MODE, 256, 256, 2, 4, true>(a, s);
+  if (m > 192 && n > 192) {
+    if constexpr (MODE != kWeightGrad) {
+      // a last round of few tiles costs as much as a full one, which matters of few rounds
+      const int64_t most = tiles_of(a, ExpertsMode(MODE), 256, 256);
+      if (most > 256 && most < 8 * 256) {
+        const hipError_t e = tiles<MODE, 256, 256, 2, 4, true, kRounds>(a, s);
+        return e == hipSuccess ? tiles<MODE, 128, 128, 2, 2, true, kQuarters>(a, s) : e;
+      }
+    }
+    return tiles<MODE, 256, 256, 2, 4, true>(a, s);
+  }
   return tiles<MODE, 128, 128, 2, 2, true>(a, s);
 }
 

@@ -50,6 +50,8 @@ CASES = {
     "one wide row": ([1], 0, 0, 4101, 24),
     "long and thin": ([2500, 0, 9], 0, 0, 45, 72),
     "long and narrow": ([0, 3333], 2, 0, 5, 6),
+    "a round and a few tiles": ([3000, 0, 257, 5100], 3, 0, 264, 2100),
+    "two rounds and a few tiles": ([9000, 255, 256], 0, 9, 72, 3600),
     "batch": ([300, 500, 0, 800, 250], 0, 50, 512, 1024),
 }
 LAYOUTS = [(0, 0), (8, 0), (64, 8), (3, 1), (0, 5)]
