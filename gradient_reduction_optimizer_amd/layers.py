@@ -28,54 +28,63 @@ _IDS = {torch.int32: B.GRO_INT32, torch.int64: B.GRO_INT64}
 
 
 def _matrix(what: str, t, device, dtypes=_TYPES) -> B.gro_matrix:
-    """A matrix of one of these types on this GPU whose rows' elements lie side by side."""
-    if t.dim() != 2 or t.dtype not in dtypes or t.device != device or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a matrix of {' or '.join(map(str, dtypes))} on {device}, rows' elements side by side, "
-                         f"is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    rows, cols = t.shape
-    return B.gro_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols, _TYPES[t.dtype], 0)
+    """A matrix of one of these types on this GPU (its index) whose rows' elements lie side by side."""
+    kind = dtypes.get(t.dtype)
+    shape = t.shape
+    if len(shape) != 2 or kind is None or t.get_device() != device or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a matrix of {' or '.join(map(str, dtypes))} on cuda:{device}, rows' elements side by "
+                         f"side, is needed, got {t.dtype} {tuple(shape)}, strides {t.stride()}, on {t.device}")
+    rows, cols = shape
+    return B.gro_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols, kind, 0)
 
 
 def _experts(what: str, t, device, dtypes=_TYPES) -> B.gro_experts:
-    if t.dim() != 3 or t.dtype not in dtypes or t.device != device or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{what}: [experts, outer, inner] of {' or '.join(map(str, dtypes))} on {device}, rows' elements side "
-                         f"by side, is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    kind = dtypes.get(t.dtype)
+    if t.dim() != 3 or kind is None or t.get_device() != device or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what}: [experts, outer, inner] of {' or '.join(map(str, dtypes))} on cuda:{device}, rows' "
+                         f"elements side by side, is needed, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on "
+                         f"{t.device}")
     n, outer, inner = t.shape
     row = t.stride(1) if outer > 1 else inner
-    return B.gro_experts(t.data_ptr(), outer, inner, row, t.stride(0) if n > 1 else outer * row, n, _TYPES[t.dtype], 0)
+    return B.gro_experts(t.data_ptr(), outer, inner, row, t.stride(0) if n > 1 else outer * row, n, kind, 0)
 
 
-def _index(what: str, t, device, dtypes, n=None) -> None:
-    if t.dim() != 1 or t.dtype not in dtypes or t.device != device or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{what}: {'' if n is None else f'{n} '}contiguous {' or '.join(map(str, dtypes))} on {device} are "
-                         f"needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _index(what: str, t, device, dtypes, n=None) -> int:
+    """The kind of a contiguous list of whole numbers on this GPU."""
+    kind = dtypes.get(t.dtype)
+    if kind is None or t.dim() != 1 or t.get_device() != device or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: {'' if n is None else f'{n} '}contiguous {' or '.join(map(str, dtypes))} on "
+                         f"cuda:{device} are needed, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return kind
 
 
-def _gpu(t) -> torch.device:
-    if t.device.type != "cuda":
+def _flat(ids):
+    return ids if ids.dim() == 1 and ids.is_contiguous() else ids.contiguous().view(-1)
+
+
+def _gpu(t) -> int:
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"the layers' tensors are on a GPU, got {t.device}")
-    return t.device
+    return device
 
 
-def _call(device, stream, tensors, made, fn, *args) -> int:
-    """fn(..., stream handle) with the tensors' device current; returns the handle.  A stream that is not the current
-    one waits for tensors that this call has ``made`` on the current one, and the tensors it uses are recorded with the
-    allocator."""
-    here = torch.cuda.current_stream(device)
-    s = here if stream is None else stream
-    if s != here:
+def _call(device, stream, tensors, made, fn, *args) -> None:
+    """fn(..., stream handle) with the tensors' GPU current.  A stream that is not the current one waits for tensors
+    that this call has ``made`` on the current one, and the tensors it uses are recorded with the allocator."""
+    s = torch.cuda.current_stream(device)
+    if stream is not None and stream != s:
         if made:
-            s.wait_stream(here)
+            stream.wait_stream(s)
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
-    handle = s.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        fn(*args, handle)
+                t.record_stream(stream)
+        s = stream
+    if torch.cuda.current_device() == device:
+        fn(*args, s.cuda_stream)
     else:
         with torch.cuda.device(device):
-            fn(*args, handle)
-    return handle
+            fn(*args, s.cuda_stream)
 
 
 def _wrote(out) -> None:
@@ -88,7 +97,7 @@ def _aligned(room) -> int:
 
 
 def _room(nbytes: int, device):
-    return torch.empty(nbytes + 256, dtype=torch.uint8, device=device) if nbytes else None
+    return torch.empty(nbytes + 256, dtype=torch.uint8, device=torch.device("cuda", device)) if nbytes else None
 
 
 def lookup(table, ids, scale: float = 1.0, first_row: int = 0, out=None, dtype=None, stream=None):
@@ -96,19 +105,17 @@ def lookup(table, ids, scale: float = 1.0, first_row: int = 0, out=None, dtype=N
     shape, the result has it with the table's width behind.  ``out``: a matrix of a row for each id, or one is
     allocated in ``dtype``, by default the table's."""
     device = _gpu(table)
-    flat = ids.contiguous().view(-1)
-    _index("ids", flat, device, _IDS)
-    if out is None:
-        rows = torch.empty((flat.numel(), table.shape[-1]), dtype=dtype or table.dtype, device=device)
-    else:
-        rows = out
+    flat = _flat(ids)
+    kind = _index("ids", flat, device, _IDS)
+    n = flat.numel()
+    rows = torch.empty((n, table.shape[-1]), dtype=dtype or table.dtype, device=table.device) if out is None else out
     m, o = _matrix("table", table, device), _matrix("out", rows, device)
-    if o.rows != flat.numel():
-        raise ValueError(f"out: {flat.numel()} rows are needed, got {o.rows}")
-    _call(device, stream, (table, flat, rows), out is None or flat.data_ptr() != ids.data_ptr(), B.gro_lookup, m, first_row,
-          flat.data_ptr(), _IDS[flat.dtype], scale, o)
+    if o.rows != n:
+        raise ValueError(f"out: {n} rows are needed, got {o.rows}")
+    _call(device, stream, (table, flat, rows), out is None or flat is not ids, B.gro_lookup, m, first_row,
+          flat.data_ptr(), kind, scale, o)
     if out is None:
-        return rows.view(*ids.shape, rows.shape[1])
+        return rows.view(*ids.shape, o.cols)
     _wrote(out)
     return out
 
@@ -122,7 +129,10 @@ class RowOrder:
 
     def __init__(self, n: int, n_rows: int, width: int = 0, device="cuda"):
         device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"the layers' tensors are on a GPU, got {device}")
         self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        self._gpu = self.device.index
         self.n, self.n_rows, self.width, self.used = int(n), int(n_rows), int(width), 0
         self._sort_bytes = B.gro_row_sort_workspace(self.n, self.n_rows)
         self._bytes = max(self._sort_bytes, B.gro_lookup_grad_workspace(self.n, self.width))
@@ -140,23 +150,22 @@ class RowOrder:
         return self._order[:self.used]
 
     def _run(self, stream, tensors, made, fn, *args) -> None:
-        handle = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-        if handle not in self._seen:
-            s = torch.cuda.current_stream(self.device) if stream is None else stream
+        s = torch.cuda.current_stream(self._gpu) if stream is None else stream
+        if s.cuda_stream not in self._seen:
             for t in (self._order, self.starts, self.workspace):
                 t.record_stream(s)
-            self._seen.add(handle)
-        _call(self.device, stream, tensors, made, fn, *args)
+            self._seen.add(s.cuda_stream)
+        _call(self._gpu, stream, tensors, made, fn, *args)
 
     def sort(self, ids, first_row: int = 0, stream=None):
         """gro_row_sort: (order, starts) of these ids, read in order of their elements."""
-        flat = ids.contiguous().view(-1)
-        _index("ids", flat, self.device, _IDS)
+        flat = _flat(ids)
+        kind = _index("ids", flat, self._gpu, _IDS)
         n = flat.numel()
         if n > self.n:
             raise ValueError(f"{n} ids, {self.n} at most")
-        self._run(stream, (flat,), flat.data_ptr() != ids.data_ptr(), B.gro_row_sort, flat.data_ptr(), _IDS[flat.dtype], n,
-                  first_row, self.n_rows, self._order.data_ptr(), self.starts.data_ptr(), self._ws, self._bytes)
+        self._run(stream, (flat,), flat is not ids, B.gro_row_sort, flat.data_ptr(), kind, n, first_row, self.n_rows,
+                  self._order.data_ptr(), self.starts.data_ptr(), self._ws, self._bytes)
         self.used = n
         return self.order, self.starts
 
@@ -167,17 +176,17 @@ class RowOrder:
         if dy.dim() < 2:
             raise ValueError(f"dy: a row for each id is needed, got {tuple(dy.shape)}")
         flat = dy if dy.dim() == 2 else dy.reshape(-1, dy.shape[-1])
-        d = _matrix("dy", flat, self.device)
+        d = _matrix("dy", flat, self._gpu)
         if accumulate and out is None:
             raise ValueError("accumulate adds to an array that is given")
         given = out is not None
         if not given:
             out = torch.empty((self.n_rows, flat.shape[1]), dtype=dtype or flat.dtype, device=self.device)
-        o = _matrix("out", out, self.device)
+        o = _matrix("out", out, self._gpu)
         if d.rows != self.used or o.rows != self.n_rows or d.cols > self.width:
             raise ValueError(f"{self.used} ids were sorted for {self.n_rows} rows of up to {self.width} elements, got "
                              f"dy {tuple(dy.shape)} and out {tuple(out.shape)}")
-        self._run(stream, (flat, out), not given or flat.data_ptr() != dy.data_ptr(), B.gro_lookup_grad, d,
+        self._run(stream, (flat, out), not given or flat is not dy, B.gro_lookup_grad, d,
                   self._order.data_ptr(), self.starts.data_ptr(), scale, bool(accumulate), o, self._ws, self._bytes)
         if given:
             _wrote(out)
@@ -194,7 +203,7 @@ def _product(fn, in_name, rows, weight, starts, out, out_name, cols, dtype, stre
     _index("starts", starts, device, _I32, w.n_experts + 1)
     given = out is not None
     if not given:  # rows that no expert has are not written by the product
-        out = torch.zeros((rows.shape[0], getattr(w, cols)), dtype=dtype or rows.dtype, device=device)
+        out = torch.zeros((rows.shape[0], getattr(w, cols)), dtype=dtype or rows.dtype, device=rows.device)
     x, y = _matrix(in_name, rows, device, _BF16), _matrix(out_name, out, device)
     nbytes = B.gro_experts_workspace(w.n_experts, x.rows, w.inner, w.outer)
     room = _room(nbytes, device)
@@ -228,7 +237,7 @@ def experts_weight_grad(dy, x, starts, out=None, accumulate: bool = False, dtype
         raise ValueError("accumulate adds to an array that is given")
     given = out is not None
     if not given:
-        out = torch.empty((max(starts.numel() - 1, 0), d.cols, r.cols), dtype=dtype or dy.dtype, device=device)
+        out = torch.empty((max(starts.numel() - 1, 0), d.cols, r.cols), dtype=dtype or dy.dtype, device=dy.device)
     w = _experts("out", out, device)
     _index("starts", starts, device, _I32, w.n_experts + 1)
     nbytes = B.gro_experts_workspace(w.n_experts, d.rows, w.inner, w.outer)

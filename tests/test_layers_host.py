@@ -163,6 +163,7 @@ def on_gpu(monkeypatch):
         fn = getattr(torch, name)
         monkeypatch.setattr(torch, name, lambda *a, device=None, fn=fn, **k: fn(*a, **k))
     monkeypatch.setattr(torch.Tensor, "device", property(lambda t: torch.device("cuda", 0)))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
     for name in ("gro_lookup", "gro_row_sort", "gro_lookup_grad", "gro_experts_forward", "gro_experts_input_grad",
