@@ -119,7 +119,7 @@ SortWorkspace sort_workspace(int64_t n, int64_t n_rows) {
 }
 
 uint64_t grad_workspace(int64_t n, int64_t cols) {
-  return up256(uint64_t(n / run_tokens(n)) * uint64_t((cols + 7) / 8 * 8) * 4);
+  return up256(uint64_t(whole_runs(n)) * uint64_t((cols + 7) / 8 * 8) * 4);
 }
 
 int check_sizes(int64_t n, int64_t other, const uint64_t* bytes, const char* what) {
@@ -334,7 +334,7 @@ extern "C" int gro_lookup_grad(const gro_matrix* dy, const int32_t* d_order, con
   a.out = device_matrix(*out);
   a.partials = static_cast<float*>(d_workspace);
   a.run = run_tokens(dy->rows);
-  a.n_runs = dy->rows / a.run;
+  a.n_runs = whole_runs(dy->rows);
   const hipError_t e = launch_lookup_grad(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GRO_OK : hip_fail(e, "lookup gradient launch");
 }

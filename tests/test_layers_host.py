@@ -64,15 +64,15 @@ def test_lookup_refuses():
 
 
 def test_lookup_grad_refuses():
-    need = B.gro_lookup_grad_workspace(100, 8)
-    ok = dict(dy=M(A, 100, 8), order=BB, starts=C, accumulate=0, out=M(D, 30, 8), ws=WS, bytes=need)
+    need = B.gro_lookup_grad_workspace(1000, 8)
+    ok = dict(dy=M(A, 1000, 8), order=BB, starts=C, accumulate=0, out=M(D, 30, 8), ws=WS, bytes=need)
 
     def grad(**k):
         a = {**ok, **k}
         B.gro_lookup_grad(a["dy"], a["order"], a["starts"], 1.0, a["accumulate"], a["out"], a["ws"], a["bytes"], 0)
 
     assert need > 0
-    for bad in (dict(dy=M(A, 100, 9)), dict(dy=M(0, 100, 8)), dict(dy=M(A, 100, 8, type=3)), dict(order=0), dict(order=BB + 1),
+    for bad in (dict(dy=M(A, 1000, 9)), dict(dy=M(0, 1000, 8)), dict(dy=M(A, 1000, 8, type=3)), dict(order=0), dict(order=BB + 1),
                 dict(starts=0), dict(starts=C + 2), dict(accumulate=2), dict(out=M(D, 30, 8, 7)), dict(out=M(A, 30, 8)),
                 dict(out=M(BB, 30, 8)), dict(out=M(C, 30, 8)), dict(out=M(D, B.GRO_MAX_TABLE_ROWS + 1, 8)), dict(ws=0),
                 dict(ws=WS + 64), dict(bytes=need - 1), dict(ws=A), dict(ws=BB), dict(ws=C), dict(ws=D)):
