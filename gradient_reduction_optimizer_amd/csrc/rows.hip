@@ -239,9 +239,10 @@ struct BucketSort {
     int digit[kRounds];
     uint32_t rank[kRounds], position[kRounds];
     const bool whole = n <= kSortTile;
-    // several tiles: the rows' totals first
+    // several tiles: the rows' totals first.  Many items may be of one row, which would
+    // hold the LDS adds up one by one: those of the wave's first item's row go as one.
     if (!whole) {
-      for (int i = int(threadIdx.x); i < kSortWaves * kBins; i += kSortBlock) counts[i] = 0;
+      for (int i = int(threadIdx.x); i < kBins; i += kSortBlock) base[i] = 0;
       __syncthreads();
       for (int64_t tile = 0; tile < n; tile += kSortTile) {
 #pragma unroll
@@ -251,11 +252,16 @@ struct BucketSort {
           if (k < n) item(k, digit[j], position[j]);
         }
 #pragma unroll
-        for (int j = 0; j < kRounds; ++j) rank_in_wave<BITS>(digit[j], mine);
+        for (int j = 0; j < kRounds; ++j) {
+          const int first = __builtin_amdgcn_readfirstlane(digit[j]);
+          const uint64_t like = __ballot(digit[j] == first);
+          if (digit[j] >= 0 && (digit[j] != first || lane == 0))
+            atomicAdd(&base[digit[j]], digit[j] == first ? uint32_t(__popcll(like)) : 1u);
+        }
       }
       __syncthreads();
       uint32_t all;
-      const uint32_t at = begin + block_prefix(prefix_over_waves(counts, kBins), part, all);
+      const uint32_t at = begin + block_prefix(int(threadIdx.x) < kBins ? base[threadIdx.x] : 0, part, all);
       if (int(threadIdx.x) < kBins) base[threadIdx.x] = at;
     }
     for (int64_t tile = 0; tile < n || (tile == 0 && whole); tile += kSortTile) {
