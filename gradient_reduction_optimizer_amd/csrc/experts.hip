@@ -80,23 +80,26 @@ struct Tiles {
     for (int e0 = 64; e0 < P.n_experts; e0 += 64)
       total += uint32_t(__builtin_amdgcn_readlane(int(prefix(count(run(P, e0 + lane)))), 63));
   }
-  __device__ __forceinline__ void find(const ExpertsLaunch& P, uint32_t tile, int& expert, int& row, int& end) const {
+  // false only for runs so many and so long, one over the other, that their tiles are not
+  // counted in 32 bits
+  __device__ __forceinline__ bool find(const ExpertsLaunch& P, uint32_t tile, int& expert, int& row, int& end) const {
     const int lane = int(threadIdx.x) & 63;
     Run q = r;
     uint32_t u = upto;
-    for (int e0 = 0;; e0 += 64) {
+    for (int e0 = 0; e0 < P.n_experts; e0 += 64) {
       const uint64_t over = __ballot(u > tile);
       if (over) {
         const int l = uniform(__ffsll(static_cast<unsigned long long>(over)) - 1);
         expert = e0 + l;
         row = __builtin_amdgcn_readlane(q.lo + int(tile - (u - count(q))) * BM, l);
         end = __builtin_amdgcn_readlane(q.hi, l);
-        return;
+        return row < end;
       }
       tile -= uint32_t(__builtin_amdgcn_readlane(int(u), 63));
       q = run(P, e0 + 64 + lane);
       u = prefix(count(q));
     }
+    return false;
   }
 };
 
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
       job.k_n = uniform(r.hi - r.lo);
     } else {
       const Place p = banded(tile, m_tiles, n_tiles);
-      tiles.find(P, p.m, job.expert, job.m0, job.m_end);
+      if (!tiles.find(P, p.m, job.expert, job.m0, job.m_end)) return false;
       job.n0 = int(p.n) * TN;
       if constexpr (QUARTERS) {
         job.m0 += int(i & 1) * BM;
@@ -607,8 +610,7 @@ __global__ __launch_bounds__(kJoinRows * BN / 4) void k_experts_join(const Exper
     if (P.accumulate && r.lo == r.hi) return;
   } else {
     const Tiles<BM> tiles(P);
-    if (tile >= tiles.total) return;
-    tiles.find(P, tile, expert, m0, m_end);
+    if (tile >= tiles.total || !tiles.find(P, tile, expert, m0, m_end)) return;
   }
   constexpr int kLanes = BN / 4;
   typedef f32x4 F4 __attribute__((aligned(4)));

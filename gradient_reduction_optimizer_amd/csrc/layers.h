@@ -67,6 +67,9 @@ struct LookupLaunch {
 };
 hipError_t launch_lookup(const LookupLaunch& a, hipStream_t s);
 
+// Columns of a gradient, 512 to a workgroup across (a grid has fewer than 2^16 that way).
+constexpr int64_t kMaxGradCols = int64_t(1) << 24;
+
 // Tokens in order are cut into runs of this many; a run within one row is summed
 // by the first launch.
 inline int64_t run_tokens(int64_t n) {

@@ -311,6 +311,8 @@ extern "C" int gro_lookup_grad(const gro_matrix* dy, const int32_t* d_order, con
                      (long long)out->cols);
   if (out->rows > kMaxTableRows)
     return set_error(GRO_E_INVALID, "%lld rows (at most %lld)", (long long)out->rows, (long long)kMaxTableRows);
+  if (out->cols > kMaxGradCols)
+    return set_error(GRO_E_INVALID, "%lld columns (at most %lld)", (long long)out->cols, (long long)kMaxGradCols);
   if (accumulate != 0 && accumulate != 1) return set_error(GRO_E_INVALID, "accumulate is 0 or 1");
   const uint64_t need = grad_workspace(dy->rows, dy->cols);
   rc = check_workspace(d_workspace, bytes, need);

@@ -535,7 +535,7 @@ int gro_lookup(const gro_matrix* table, int64_t first_row, const void* d_ids, in
  * r's positions i.  Every row is written, zeros for rows without any; with
  * accumulate = 1 it is added to what is there, and rows without any are not touched
  * (a tied head's gradient, an FP32 gradient of several microbatches).  Sums are
- * FP32, rounded once.  dy and out are BF16 or FP32 each.  Entries of d_order and
+ * FP32, rounded once.  dy and out are BF16 or FP32 each, of at most 2^24 columns.  Entries of d_order and
  * d_starts outside their range are never followed. */
 int gro_lookup_grad_workspace(int64_t n, int64_t cols, uint64_t* bytes);
 int gro_lookup_grad(const gro_matrix* dy, const int32_t* d_order, const int32_t* d_starts, double scale,

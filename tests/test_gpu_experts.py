@@ -159,6 +159,20 @@ def test_starts_out_of_range_are_cut():
     assert bool((dw[1] == 0).all()) and bool((dw[3] == 0).all())
 
 
+def test_runs_over_each_other_end_and_stay_inside():
+    """Starts that go up and down give runs over each other, more tiles than rows could have: whatever the rows
+    hold then, the calls end and write nothing outside."""
+    n, rows = 130, 300
+    starts = torch.tensor([0, rows] * (n // 2) + [0], dtype=torch.int32).cuda()
+    for inner, outer in ((64, 72), (512, 40)):
+        x, w = normal(1, rows, inner).cuda(), normal(2, n, outer, inner).cuda()
+        out = R.Matrix(torch.zeros(rows, outer, dtype=F32), 4)
+        L.experts_forward(x, w, starts, out=out.view)
+        back = R.Matrix(torch.zeros(rows, inner, dtype=F32), 4)
+        L.experts_input_grad(normal(3, rows, outer).cuda(), w, starts, out=back.view)
+        assert out.rest_untouched() and back.rest_untouched()
+
+
 def test_columns_side_by_side_in_one_matrix():
     """Input and result as two halves of one matrix's columns, weights as the halves of each expert's rows."""
     c = Case("eights")

@@ -74,8 +74,8 @@ def test_lookup_grad_refuses():
     assert need > 0
     for bad in (dict(dy=M(A, 1000, 9)), dict(dy=M(0, 1000, 8)), dict(dy=M(A, 1000, 8, type=3)), dict(order=0), dict(order=BB + 1),
                 dict(starts=0), dict(starts=C + 2), dict(accumulate=2), dict(out=M(D, 30, 8, 7)), dict(out=M(A, 30, 8)),
-                dict(out=M(BB, 30, 8)), dict(out=M(C, 30, 8)), dict(out=M(D, B.GRO_MAX_TABLE_ROWS + 1, 8)), dict(ws=0),
-                dict(ws=WS + 64), dict(bytes=need - 1), dict(ws=A), dict(ws=BB), dict(ws=C), dict(ws=D)):
+                dict(out=M(BB, 30, 8)), dict(out=M(C, 30, 8)), dict(out=M(D, B.GRO_MAX_TABLE_ROWS + 1, 8)),
+                dict(dy=M(A, 1, (1 << 24) + 1), out=M(D, 1, (1 << 24) + 1), bytes=1 << 40), dict(ws=0), dict(ws=WS + 64), dict(bytes=need - 1), dict(ws=A), dict(ws=BB), dict(ws=C), dict(ws=D)):
         refused(lambda bad=bad: grad(**bad))
 
 
