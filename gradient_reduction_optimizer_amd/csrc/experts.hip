@@ -273,30 +273,25 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
-// N neighbours of a row of C, of which `left` exist: four, or in BF16 eight too.
-template <bool CF, int N>
-__device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int left, const float (&x)[N]) {
+// Four neighbours of a row of C, or eight that are rounded already, of which `left`
+// exist.
+template <bool CF>
+__device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int left, f32x4 x) {
   typedef f32x4 F4 __attribute__((aligned(4)));
-  typedef uint16_t Bf16 __attribute__((ext_vector_type(N)));
-  typedef Bf16 Bf16Any __attribute__((aligned(2)));
-  if (left >= N) {
+  typedef u32x2 B4 __attribute__((aligned(2)));
+  if (left >= 4) {
     if constexpr (CF) {
-      static_assert(N == 4, "16 bytes");
       F4* c = reinterpret_cast<F4*>(static_cast<float*>(P.c) + at);
-      f32x4 y = {x[0], x[1], x[2], x[3]};
-      if (P.accumulate) y += *c;
-      __builtin_nontemporal_store(y, c);
+      if (P.accumulate) x += *c;
+      *c = x;
     } else {
-      Bf16Any* c = reinterpret_cast<Bf16Any*>(static_cast<uint16_t*>(P.c) + at);
-      Bf16 y = {};
-      if (P.accumulate) y = *c;
-#pragma unroll
-      for (int e = 0; e < N; ++e) y[e] = bf16_bits(P.accumulate ? widen1(y[e]) + x[e] : x[e]);
-      __builtin_nontemporal_store(y, c);
+      B4* c = reinterpret_cast<B4*>(static_cast<uint16_t*>(P.c) + at);
+      if (P.accumulate) x += widen4(*c);
+      *c = u32x2{bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3])};
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+    for (int e = 0; e < 3; ++e)
       if (e < left) {
         if constexpr (CF) {
           float* c = static_cast<float*>(P.c) + at + e;
@@ -306,6 +301,19 @@ __device__ __forceinline__ void store_c(const ExpertsLaunch& P, int64_t at, int 
           *c = bf16_bits(P.accumulate ? widen1(*c) + x[e] : x[e]);
         }
       }
+  }
+}
+template <bool LINES>
+__device__ __forceinline__ void store_rounded(const ExpertsLaunch& P, int64_t at, int left, u16x8 x) {
+  typedef u16x8 B8 __attribute__((aligned(2)));
+  uint16_t* c = static_cast<uint16_t*>(P.c) + at;
+  if (left >= 8) {
+    if constexpr (LINES) __builtin_nontemporal_store(x, reinterpret_cast<B8*>(c));
+    else *reinterpret_cast<B8*>(c) = x;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < left) c[e] = x[e];
   }
 }
 
@@ -346,10 +354,17 @@ __device__ __forceinline__ uint32_t left_over(uint32_t total) {
   return total > 256 && n <= 128 ? n : 0;
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER, bool CF>
+// C in FP32, in BF16, or in BF16 with rows that begin at whole lines of 128 bytes.  The
+// last are stored past the caches, since C is larger than they are and the next tiles'
+// operands are in them: an input gradient of 16,384 rows 136 us instead of 157.  Pieces
+// of lines are left to the caches: 48 weight gradients of 1408 x 3944 without a row each
+// 199 us instead of 345.  FP32 takes the same time either way.
+enum Result { kFp32, kBf16, kBf16Lines };
+
+template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER, int C>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const ExpertsLaunch P) {
   constexpr int kThreads = 64 * WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
-  constexpr bool PARTS = COVER == kParts, QUARTERS = COVER == kQuarters;
+  constexpr bool CF = C == kFp32, PARTS = COVER == kParts, QUARTERS = COVER == kQuarters;
   constexpr int TM = QUARTERS ? 2 * BM : BM, TN = QUARTERS ? 2 * BN : BN;  // as tiles are numbered
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
   constexpr uint32_t kChunk = 32 * tile_units(BM, BN, WM * WN), kGrid = 8 * kChunk;
@@ -430,10 +445,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     return false;
   };
 
-  constexpr int kWide = CF ? 4 : 8, kLanes = 32 / kWide, kRows = 64 / kLanes;
+  static_assert(FN == 2, "a wave's block of results is 64 wide");
   Loader<DIRECT, AT, BM, kThreads> la;
   Loader<DIRECT, BT, BN, kThreads> lb;
-  constexpr int kLoads = decltype(la)::L::kLoads + decltype(lb)::L::kLoads, kStores = FM * FN * 32 / kRows;
+  constexpr int kLoads = decltype(la)::L::kLoads + decltype(lb)::L::kLoads, kStores = CF ? 8 * FM : 4 * FM;
   static_assert((kStages - 1) * kLoads + kStores < 64, "vmcnt counts to 63");
   Reader<AT, BM, FM> ra;
   Reader<BT, BN, FN> rb;
@@ -537,7 +552,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
         if (++s >= steps) break;
       }
     }
-    step_barrier<0>();
+    // the buffers are free; they are anyway where nothing was to be summed, and then the
+    // stores of the tile before need not be waited for
+    if (job.k_n > 0) step_barrier<0>();
     if (left > 0) {
       la.copy_part(a0, left);
       lb.copy_part(b0, left);
@@ -551,17 +568,42 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
     const Job done = job;
     job = ahead;
     if (more) begin(job);
-    stored = done.m0 + BM <= done.m_end && done.n0 + BN <= n_end;
+    stored = done.m0 + BM <= done.m_end && done.n0 + BN <= n_end;  // kStores by every wave, or more
 
-    // Lane l has row l mod 32 of a block of C and of its columns four times four, 8 q +
-    // 4 * (l / 32) on.  32 x 32 at a time go through the wave's own LDS, row r's chunk c of
-    // four at place c ^ (r / 2 mod 8), and from there to memory in pieces of whole rows.
     if (MODE == kWeightGrad && P.accumulate && done.k_n == 0) {
       stored = false;
       continue;
     }
     const int64_t base = (MODE == kWeightGrad ? done.expert * P.c_expert : 0) + (PARTS ? done.part * P.c_part : 0);
+    // Lane l has row l mod 32 of a block of 32 x 32 of C and of its columns four times
+    // four, 8 q + 4 * (l / 32) on.  They go through the wave's own LDS, row r's chunk c of
+    // 16 bytes at place c ^ (r / 2 mod 8), and from there to memory in whole lines of 128
+    // bytes: 32 columns in FP32, or 64 that are rounded first, unless something is added.
     float* block = results[wave];
+    if (!CF && !P.accumulate) {
+      uint16_t* rounded = reinterpret_cast<uint16_t*>(block);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = lane & 31, c = (4 * j + q) ^ ((r >> 1) & 7);
+            *reinterpret_cast<u32x2*>(rounded + r * 64 + 8 * c + 4 * (lane >> 5)) =
+                u32x2{bf16x2_bits(acc[i][j][4 * q], acc[i][j][4 * q + 1]), bf16x2_bits(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+          }
+        in_wave_order();
+        const int n = done.n0 + wn + lane % 8 * 8;
+#pragma unroll
+        for (int t = 0; t < 32; t += 8) {
+          const int r = t + lane / 8, m = done.m0 + wm + 32 * i + r;
+          const u16x8 x = *reinterpret_cast<const u16x8*>(rounded + r * 64 + 8 * (lane % 8 ^ ((r >> 1) & 7)));
+          if (m < done.m_end && n < n_end) store_rounded<C == kBf16Lines>(P, base + m * P.c_stride + n, n_end - n, x);
+        }
+        in_wave_order();
+      }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -573,18 +615,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
         }
         in_wave_order();
-        const int n = done.n0 + wn + 32 * j + lane % kLanes * kWide;
+        const int n = done.n0 + wn + 32 * j + lane % 8 * 4;
 #pragma unroll
-        for (int t = 0; t < 32; t += kRows) {
-          const int r = t + lane / kLanes, m = done.m0 + wm + 32 * i + r;
-          float x[kWide];
-#pragma unroll
-          for (int h = 0; h < kWide / 4; ++h) {
-            const f32x4 v = ld4f(block + r * 32 + 4 * ((lane % kLanes * (kWide / 4) + h) ^ ((r >> 1) & 7)));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
-          }
-          if (m < done.m_end && n < n_end) store_c<CF, kWide>(P, base + m * P.c_stride + n, n_end - n, x);
+        for (int t = 0; t < 32; t += 8) {
+          const int r = t + lane / 8, m = done.m0 + wm + 32 * i + r;
+          const f32x4 x = ld4f(block + r * 32 + 4 * (lane % 8 ^ ((r >> 1) & 7)));
+          if (m < done.m_end && n < n_end) store_c<CF>(P, base + m * P.c_stride + n, n_end - n, x);
         }
         in_wave_order();
       }
@@ -618,7 +654,7 @@ __global__ __launch_bounds__(kJoinRows * BN / 4) void k_experts_join(const Exper
   const int m = m0 + int(blockIdx.x % (BM / kJoinRows)) * kJoinRows + int(threadIdx.x) / kLanes;
   if (left <= 0 || m >= m_end) return;
   const float* p = P.partials + (MODE == kWeightGrad ? int64_t(expert) * P.outer * P.inner : 0) + int64_t(m) * n_end + n;
-  float x[4] = {};
+  f32x4 x = {};
 #pragma unroll 8
   for (int part = 0; part < P.n_parts; ++part, p += P.c_part) {
     f32x4 y = {};
@@ -629,10 +665,9 @@ __global__ __launch_bounds__(kJoinRows * BN / 4) void k_experts_join(const Exper
       for (int e = 0; e < 3; ++e)
         if (e < left) y[e] = p[e];
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] += y[e];
+    x += y;
   }
-  store_c<CF, 4>(P, (MODE == kWeightGrad ? expert * P.c_expert : 0) + m * P.c_stride + n, left, x);
+  store_c<CF>(P, (MODE == kWeightGrad ? expert * P.c_expert : 0) + m * P.c_stride + n, left, x);
 }
 
 // Tiles of BM x BN that cover C: every expert's last one may be a part of one.
@@ -658,8 +693,10 @@ hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(BM, BN, WM * WN);
   const uint32_t n = COVER == kQuarters ? 256 * units : xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
   const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
-  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, false>), grid, block, 0, s, a);
+  const bool lines = ((reinterpret_cast<uintptr_t>(a.c) | uint64_t(2 * a.c_stride) | uint64_t(2 * a.c_expert)) & 127) == 0;
+  if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, kFp32>), grid, block, 0, s, a);
+  else if (DIRECT && lines) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, DIRECT ? kBf16Lines : kBf16>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, kBf16>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -675,7 +712,7 @@ hipError_t in_parts(const ExpertsLaunch& a, hipStream_t s) {
   constexpr uint32_t units = tile_units(128, 128, 4);
   const uint32_t n = uint32_t(tiles_of(a, ExpertsMode(MODE), 128, 128));
   const dim3 places(std::min(xcd_numbers(n * uint32_t(a.n_parts), 32 * units), 256 * units)), grid(n * (128 / kJoinRows));
-  hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, kParts, true>), places, dim3(256), 0, s, b);
+  hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, kParts, kFp32>), places, dim3(256), 0, s, b);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.c_fp32) hipLaunchKernelGGL((k_experts_join<MODE, 128, 128, true>), grid, dim3(kJoinRows * 32), 0, s, a);
@@ -688,19 +725,23 @@ hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
   const bool whole = direct(a, ExpertsMode(MODE));
   if (a.n_parts > 1) return whole ? in_parts<MODE, true>(a, s) : in_parts<MODE, false>(a, s);
   if (!whole) return tiles<MODE, 128, 128, 2, 2, false>(a, s);
+  // Large tiles where an expert's rows and its columns of C are most of one and three
+  // quarters of the GPU have one.  us, large against small, 16 experts from 2048 to 2048:
+  // 64 rows each 45 / 26, 128 46 / 27, 256 51 / 47, 384 70 / 81, 512 69 / 86; 8 experts of
+  // 2048 rows from 1024 to 256, 64 large tiles: 27 / 15.
   const int64_t n = MODE == kForward ? a.outer : a.inner, m = MODE == kWeightGrad ? a.outer : a.rows / a.n_experts;
-  if (m > 192 && n > 192) {
-    if constexpr (MODE != kWeightGrad) {
-      // a last round of few tiles costs as much as a full one, which matters of few rounds
-      const int64_t most = tiles_of(a, ExpertsMode(MODE), 256, 256);
-      if (most > 256 && most < 8 * 256) {
-        const hipError_t e = tiles<MODE, 256, 256, 2, 4, true, kRounds>(a, s);
-        return e == hipSuccess ? tiles<MODE, 128, 128, 2, 2, true, kQuarters>(a, s) : e;
-      }
+  const int64_t most = tiles_of(a, ExpertsMode(MODE), 256, 256);
+  if (m <= 192 || n <= 192 || most < 192) return tiles<MODE, 128, 128, 2, 2, true>(a, s);
+  if constexpr (MODE != kWeightGrad) {
+    // A last round of few tiles costs as much as a full one.  us, all in large tiles
+    // against quarters for those, 2048 to 2048: 8,448 rows 104 / 84, 16,896 164 / 146,
+    // 33,280 279 / 266, 66,048 539 / 527, 131,584 1,081 / 1,082.
+    if (most > 256 && most < 16 * 256) {
+      const hipError_t e = tiles<MODE, 256, 256, 2, 4, true, kRounds>(a, s);
+      return e == hipSuccess ? tiles<MODE, 128, 128, 2, 2, true, kQuarters>(a, s) : e;
     }
-    return tiles<MODE, 256, 256, 2, 4, true>(a, s);
   }
-  return tiles<MODE, 128, 128, 2, 2, true>(a, s);
+  return tiles<MODE, 256, 256, 2, 4, true>(a, s);
 }
 
 }  // namespace
@@ -708,7 +749,10 @@ hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
 int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode) { return tiles_of(a, mode, 128, 128); }
 
 // Parts that the sums over k are cut into where there are few tiles for the GPU's 512
-// places of 128 x 128: each of 8 steps or more.
+// places of 128 x 128, each of 8 steps or more: where the steps that a workgroup saves
+// (0.2 us each) are more than the join costs (5 us and the parts' traffic).  us, whole
+// against parts, to 1024: 128 rows of one expert from 4096 30 / 15, from 1024 11.5 / 13.4
+// (so whole); 16 rows each of 4 experts from 2048 17 / 13, of 16 experts 18 / 22 (whole).
 int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inner, int64_t outer) {
   if (n_experts <= 0 || rows <= 0 || inner <= 0 || outer <= 0) return 1;
   ExpertsLaunch a = {};
@@ -717,8 +761,8 @@ int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inn
   a.inner = inner;
   a.outer = outer;
   const int64_t k = mode == kForward ? inner : mode == kInputGrad ? outer : rows / n_experts;
-  const int64_t parts = std::min(512 / tiles_of(a, mode, 128, 128), k / (8 * kStepK));
-  return int(std::min<int64_t>(std::max<int64_t>(parts, 1), 32));
+  const int64_t steps = k / kStepK, parts = std::min<int64_t>(std::min(512 / tiles_of(a, mode, 128, 128), steps / 8), 32);
+  return parts > 1 && steps * (parts - 1) >= 52 * parts ? int(parts) : 1;
 }
 
 hipError_t launch_experts(const ExpertsLaunch& a, ExpertsMode mode, hipStream_t s) {
