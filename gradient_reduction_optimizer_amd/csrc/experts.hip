@@ -108,7 +108,7 @@ struct Tiles {
 // every wave sums 128 x 64 (or 64 x 64) of C in registers, from fragments of 32 x 16.
 //   Copies.  Both operands' tiles go from global memory to one of four buffers in LDS
 // without passing registers (or, at other alignments, through them), three steps ahead
-// of their use: a step takes 0.5 us, a read from memory up to 2.  Waves wait for the
+// of their use: a step takes 0.8 us, a read from memory up to 2.  Waves wait for the
 // copies of the next step only, by counting their accesses.
 //   One barrier a step.  Every wave reads the fragments of half a step while it
 // multiplies those of the half before, so at the barrier all reads of a buffer are done

@@ -18,9 +18,7 @@ struct Matrix {
 };
 
 // ------------------------------------------------------------- positions by row
-// Rows belong to buckets of 64, 256 or 1024 consecutive ones, which one workgroup
-// sorts: as few rows as give up to 256 or kMaxBuckets buckets (8,192 ids of 16,384 rows
-// in buckets of 64 9.3 us, of 256 10.2).
+// Rows belong to buckets of 2^bits consecutive ones, which one workgroup sorts.
 constexpr int64_t kMaxTableRows = int64_t(1) << 20;
 constexpr int64_t kMaxIds = (int64_t(1) << 31) - (1 << 16);
 constexpr int kMaxBuckets = 1024;
@@ -29,8 +27,20 @@ constexpr int kMaxBuckets = 1024;
 // 16 for three launches of a few more.
 constexpr int kSortTile = 8192;
 
-inline int bucket_bits(int64_t n_rows) {
-  return n_rows <= int64_t(256) << 6 ? 6 : n_rows <= int64_t(kMaxBuckets) << 8 ? 8 : 10;
+inline int bucket_bits(int64_t n, int64_t n_rows) {
+  // One launch, in which every workgroup reads all ids: up to 256 of them (8,192 ids of
+  // 16,384 rows in buckets of 64 9.3 us, of 256 10.2).
+  if (n <= kSortTile) return n_rows <= int64_t(256) << 6 ? 6 : n_rows <= int64_t(kMaxBuckets) << 8 ? 8 : 10;
+  // Few rows: buckets of one row end the sort with the second launch of three, however
+  // uneven the rows are (262,144 ids of 64 rows 14 us instead of 410 in one bucket, of
+  // 1,024 rows 19 instead of 42).
+  if (n_rows <= kMaxBuckets) return 0;
+  // More: up to 512 buckets.  The second launch's workgroups all read every chunk's
+  // counts of all of them, the third's take about the same time each (262,144 ids of
+  // 4,000 rows in 1,000 buckets 27 us, 250 20, 63 23; of 262,144 rows in 1,024 35, 256 22).
+  int bits = 2;
+  while (bits < 10 && n_rows > int64_t(512) << bits) bits += 2;
+  return bits;
 }
 
 struct RowSortLaunch {

@@ -108,11 +108,11 @@ struct SortWorkspace {
 SortWorkspace sort_workspace(int64_t n, int64_t n_rows) {
   SortWorkspace w;
   if (n <= kSortTile) return w;
-  const int bits = bucket_bits(n_rows);
+  const int bits = bucket_bits(n, n_rows);
   w.n_buckets = int32_t(std::max<int64_t>(1, (n_rows + (int64_t(1) << bits) - 1) >> bits));
   w.chunk = sort_chunk(n);
   w.n_chunks = int32_t((n + w.chunk - 1) / w.chunk);
-  w.counts = up256(uint64_t(n) * 8);
+  w.counts = bits > 0 ? up256(uint64_t(n) * 8) : 0;
   w.bases = w.counts + up256(uint64_t(w.n_chunks) * uint64_t(w.n_buckets) * 4);
   w.total = w.bases + up256(uint64_t(w.n_buckets + 1) * 4);
   return w;

@@ -334,19 +334,26 @@ __global__ __launch_bounds__(kSortBlock) void k_row_sort_few(const RowSortLaunch
 // More ids, first launch: how many of each chunk belong to each bucket.
 __global__ __launch_bounds__(kSortBlock) void k_row_sort_count(const RowSortLaunch P, const int bits) {
   __shared__ uint32_t counts[kMaxBuckets];
+  const int lane = int(threadIdx.x) & 63;
   counts[threadIdx.x] = 0;
   __syncthreads();
   const int64_t lo = int64_t(blockIdx.x) * P.chunk, hi = std::min(lo + P.chunk, P.n);
 #pragma unroll 4
   for (int64_t i = lo + threadIdx.x; i < hi; i += kSortBlock) {
     const uint32_t r = row_of_id(P.ids, P.wide_ids, i, P.first, P.n_rows);
-    if (r != 0xffffffffu) atomicAdd(&counts[r >> bits], 1u);
+    const uint32_t bucket = r >> bits;
+    // many may be of one bucket: the wave's first item's go as one
+    const uint32_t head = __builtin_amdgcn_readfirstlane(bucket);
+    const uint64_t like = __ballot(r != 0xffffffffu && bucket == head);
+    if (r != 0xffffffffu && (bucket != head || (like & ((uint64_t(1) << lane) - 1)) == 0))
+      atomicAdd(&counts[bucket], bucket == head ? uint32_t(__popcll(like)) : 1u);
   }
   __syncthreads();
   if (int(threadIdx.x) < P.n_buckets) P.counts[int64_t(blockIdx.x) * P.n_buckets + threadIdx.x] = counts[threadIdx.x];
 }
 
-// Second launch: rows and positions to their buckets, in order.
+// Second launch: rows and positions to their buckets, in order; positions to their rows
+// where every row is a bucket, which ends the sort.
 __global__ __launch_bounds__(kSortBlock) void k_row_sort_spread(const RowSortLaunch P, const int bits) {
   constexpr int kRounds = kSortChunk / kSortBlock;
   __shared__ uint32_t counts[kSortWaves * kMaxBuckets];
@@ -378,8 +385,13 @@ __global__ __launch_bounds__(kSortBlock) void k_row_sort_spread(const RowSortLau
   const uint32_t begin = block_prefix(total, part, all);
   base[threadIdx.x] = begin + before;
   if (blockIdx.x == 0) {
-    if (int(threadIdx.x) < nb) P.bases[threadIdx.x] = begin;
-    if (threadIdx.x == 0) P.bases[nb] = all;
+    if (bits > 0) {
+      if (int(threadIdx.x) < nb) P.bases[threadIdx.x] = begin;
+      if (threadIdx.x == 0) P.bases[nb] = all;
+    } else {
+      if (int64_t(threadIdx.x) < P.n_rows) P.starts[threadIdx.x] = int32_t(begin);
+      if (threadIdx.x == 0) P.starts[P.n_rows] = int32_t(all);
+    }
   }
   const int64_t lo = int64_t(blockIdx.x) * P.chunk, hi = std::min(lo + P.chunk, P.n);
   const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
@@ -405,7 +417,8 @@ __global__ __launch_bounds__(kSortBlock) void k_row_sort_spread(const RowSortLau
       if (digit[j] >= 0) {
         const int64_t to = base[digit[j]] + counts[wave * nb + digit[j]] + rank[j];
         const uint32_t position = uint32_t(tile + wave * 64 * kRounds + j * 64 + lane);
-        *reinterpret_cast<u32x2*>(P.pairs + 2 * to) = u32x2{row[j], position};
+        if (bits > 0) *reinterpret_cast<u32x2*>(P.pairs + 2 * to) = u32x2{row[j], position};
+        else P.order[to] = int32_t(position);
       }
     __syncthreads();
     base[threadIdx.x] += here;
@@ -691,7 +704,7 @@ void sort_few(const RowSortLaunch& a, dim3 grid, hipStream_t s) {
 static_assert(kSortTile == 8 * kSortBlock, "the longest list of one launch");
 
 hipError_t launch_row_sort(const RowSortLaunch& a, hipStream_t s) {
-  const int bits = bucket_bits(a.n_rows);
+  const int bits = bucket_bits(a.n, a.n_rows);
   // a table without rows has one (empty) bucket, which stores starts[0]
   const dim3 buckets(unsigned(std::max<int64_t>(1, (a.n_rows + (int64_t(1) << bits) - 1) >> bits)));
   if (a.n <= kSortTile) {
@@ -705,8 +718,10 @@ hipError_t launch_row_sort(const RowSortLaunch& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_row_sort_spread, dim3(unsigned(a.n_chunks)), dim3(kSortBlock), 0, s, a, bits);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (bits == 6) hipLaunchKernelGGL(k_row_sort_bucket<6>, buckets, dim3(kSortBlock), 0, s, a);
+  if (e != hipSuccess || bits == 0) return e;
+  if (bits == 2) hipLaunchKernelGGL(k_row_sort_bucket<2>, buckets, dim3(kSortBlock), 0, s, a);
+  else if (bits == 4) hipLaunchKernelGGL(k_row_sort_bucket<4>, buckets, dim3(kSortBlock), 0, s, a);
+  else if (bits == 6) hipLaunchKernelGGL(k_row_sort_bucket<6>, buckets, dim3(kSortBlock), 0, s, a);
   else if (bits == 8) hipLaunchKernelGGL(k_row_sort_bucket<8>, buckets, dim3(kSortBlock), 0, s, a);
   else hipLaunchKernelGGL(k_row_sort_bucket<10>, buckets, dim3(kSortBlock), 0, s, a);
   return hipGetLastError();

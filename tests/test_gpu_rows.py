@@ -43,7 +43,8 @@ def draw_ids(n, rows, seed, kind="mixed", first=0, dtype=torch.int64):
 
 SORTS = [(0, 5), (0, 0), (1, 0), (1, 1), (2, 1), (63, 64), (64, 64), (65, 256), (1000, 257), (1024, 255), (4095, 64),
          (4096, 1000), (8191, 513), (8192, 16_384), (8193, 16_384), (8193, 0), (8200, 1), (12_288, 33), (20_001, 32_000),
-         (70_000, 262_144), (70_000, 262_145), (5_000, 1_048_576), (100_003, 1_048_576)]
+         (70_000, 262_144), (70_000, 262_145), (5_000, 1_048_576), (100_003, 1_048_576), (8193, 64), (20_000, 1024),
+         (20_000, 1025), (300_000, 16), (1_100_000, 1000), (1_100_000, 40_000)]
 
 
 @pytest.mark.parametrize("n,rows", SORTS)
