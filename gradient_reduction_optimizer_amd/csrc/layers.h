@@ -83,18 +83,20 @@ hipError_t launch_lookup(const LookupLaunch& a, hipStream_t s);
 // Columns of a gradient, 512 to a workgroup across (a grid has fewer than 2^16 that way).
 constexpr int64_t kMaxGradCols = int64_t(1) << 24;
 
+constexpr int64_t kShortRun = 16, kMaxRuns = 4096, kRunsFrom = 512;
+
 // Tokens in order are cut into runs of this many; a run within one row is summed
 // by the first launch (without it a row that has all of 65,536 tokens is one
 // workgroup's work).
 inline int64_t run_tokens(int64_t n) {
-  int64_t c = 16;
-  while (c * 4096 < n) c *= 2;
+  int64_t c = kShortRun;
+  while (c * kMaxRuns < n) c *= 2;
   return c;
 }
 
 // Runs of so many tokens; few tokens do without (the second launch alone takes 5 us
 // instead of 7 for both at 37 of them).
-inline int64_t whole_runs(int64_t n) { return n < 512 ? 0 : n / run_tokens(n); }
+inline int64_t whole_runs(int64_t n) { return n < kRunsFrom ? 0 : n / run_tokens(n); }
 
 struct LookupGradLaunch {
   Matrix dy;

@@ -113,13 +113,17 @@ SortWorkspace sort_workspace(int64_t n, int64_t n_rows) {
   w.chunk = sort_chunk(n);
   w.n_chunks = int32_t((n + w.chunk - 1) / w.chunk);
   w.counts = bits > 0 ? up256(uint64_t(n) * 8) : 0;
-  w.bases = w.counts + up256(uint64_t(w.n_chunks) * uint64_t(w.n_buckets) * 4);
+  // chunks as short as the shorter lists' that a caller may sort in the same workspace
+  const uint64_t chunks = uint64_t(std::min<int64_t>((n + kSortChunk - 1) / kSortChunk, kMaxSortChunks));
+  w.bases = w.counts + up256(chunks * uint64_t(w.n_buckets) * 4);
   w.total = w.bases + up256(uint64_t(w.n_buckets + 1) * 4);
   return w;
 }
 
 uint64_t grad_workspace(int64_t n, int64_t cols) {
-  return up256(uint64_t(whole_runs(n)) * uint64_t((cols + 7) / 8 * 8) * 4);
+  // as many runs as any list of up to n ids has
+  const int64_t runs = n < kRunsFrom ? 0 : std::min<int64_t>(n / kShortRun, kMaxRuns);
+  return up256(uint64_t(runs) * uint64_t((cols + 7) / 8 * 8) * 4);
 }
 
 int check_sizes(int64_t n, int64_t other, const uint64_t* bytes, const char* what) {

@@ -518,7 +518,8 @@ typedef struct gro_matrix {
  * values are left out.  Also gives experts' runs of rows: ids = a router's choices,
  * n_rows = the number of experts.
  * d_ids: GRO_INT32 or GRO_INT64 (id_type); n < 2^31 - 2^16.  The workspace (256-byte
- * aligned) has the bytes that gro_row_sort_workspace gives, 0 for short lists. */
+ * aligned) has the bytes that gro_row_sort_workspace gives, 0 for short lists; shorter
+ * lists need no more. */
 int gro_row_sort_workspace(int64_t n, int64_t n_rows, uint64_t* bytes);
 int gro_row_sort(const void* d_ids, int32_t id_type, int64_t n, int64_t first_row, int64_t n_rows,
                  int32_t* d_order, int32_t* d_starts, void* d_workspace, uint64_t bytes, void* stream);

@@ -323,3 +323,36 @@ def test_an_embedding_and_experts_through_a_step():
         B.gro_clip_adamw(plan.handle, st.acc.data_ptr(), 1, 1.0, hp, step, st.master.data_ptr(), st.m.data_ptr(),
                          st.v.data_ptr(), st.p_bf16.data_ptr(), s)
         assert not torch.equal(before, st.p_bf16)
+
+
+def test_places_past_32_bits():
+    """Operands and results whose rows or experts lie more than 2^32 bytes apart; whole numbers, exact in FP32."""
+    r = torch.Generator().manual_seed(77)
+    few = lambda *shape: torch.randint(-2, 3, shape, generator=r).to(BF16)  # noqa: E731
+    n, inner, outer = 1_100_000, 8, 2048
+    starts = torch.tensor([0, 3, 700_001, n], dtype=torch.int32).cuda()
+    room = torch.zeros(3, 1_300_000_000, dtype=BF16, device="cuda")
+    w = room[:, -outer * inner:].view(3, outer, inner)
+    w.copy_(few(3, outer, inner))
+    x = few(n, inner).cuda()
+    y = L.experts_forward(x, w, starts)
+    at = [0, 3, 700_001, n]
+    for e in range(3):
+        for lo in range(at[e], at[e + 1], 100_000):
+            hi = min(lo + 100_000, at[e + 1])
+            assert torch.equal(y[lo:hi].float(), x[lo:hi].float() @ w[e].float().t())    # at most 32: exact in BF16
+    # rows of 4.5 GB as dy: sums over 2048 products up to 64, below 2^24
+    dx = L.experts_input_grad(y, w, starts, dtype=F32)
+    for lo, hi, e in ((0, 3, 0), (600_000, 700_001, 1), (n - 100_000, n, 2)):
+        assert torch.equal(dx[lo:hi].double(), y[lo:hi].double() @ w[e].double())
+    # rows 120,000 elements apart as x and their gradients' experts as far as the weights'; the last expert's 20 rows
+    m = 20_000
+    far = torch.zeros(m, 120_000, dtype=BF16, device="cuda")[:, :64]
+    far.copy_(few(m, 64))
+    dy = few(m, 128).cuda()
+    s2 = torch.tensor([0, 10_000, m - 20, m], dtype=torch.int32).cuda()
+    dw = room[:, :128 * 64].view(3, 128, 64)
+    L.experts_weight_grad(dy, far, s2, out=dw)
+    for e, (lo, hi) in enumerate(((0, 10_000), (10_000, m - 20), (m - 20, m))):
+        want = dy[lo:hi].double().t() @ far[lo:hi].double()
+        assert torch.equal(dw[e], want.to(BF16))               # FP32 sums below 2^24 are exact, rounded once

@@ -229,3 +229,38 @@ def test_another_stream_than_the_current_one():
     assert torch.equal(got, want)
     mine = (ids[::2] >= 0) & (ids[::2] < rows)
     assert torch.equal(looked, torch.where(mine[:, None], want[ids[::2].clamp(0, rows - 1)], 0))
+
+
+@pytest.mark.parametrize("most,rows,lengths", [(70_000, 300, (65_536, 511, 8192, 70_000)),
+                                               (1_048_600, 1000, (1_048_576, 12_288, 3)),
+                                               (1_048_600, 1025, (1_048_576, 8193))])
+def test_one_row_order_for_shorter_lists(most, rows, lengths):
+    by = RowOrder(most, rows, 4)
+    dy = torch.randint(-3, 4, (most, 4), generator=gen(most)).to(BF16)
+    for n in lengths:
+        ids = draw_ids(n, rows, n, "mixed")
+        want, starts = R.row_order(ids, 0, rows)
+        order, got = by.sort(ids.cuda())
+        assert np.array_equal(order[:len(want)].cpu().numpy(), want) and np.array_equal(got.cpu().numpy(), starts)
+        inside = (ids >= 0) & (ids < rows)
+        sums = torch.zeros(rows, 4, dtype=F64).index_add_(0, ids[inside].long(), dy[:n][inside].to(F64))
+        out = by.lookup_grad(dy[:n].cuda(), dtype=F32)
+        assert torch.equal(out.to(F64).cpu(), sums)         # whole numbers below 2^24: exact in FP32
+
+
+def test_places_past_32_bits():
+    """Results of more than 2^31 elements, 4.5 GB, and rows of a table that lie as far apart."""
+    n, rows, width = 1_100_000, 5, 2048
+    big = torch.empty(rows, 600_000_000, dtype=BF16, device="cuda")
+    table = big[:, -width:]
+    table.copy_(torch.randint(-2, 3, (rows, width), generator=gen(3)).to(BF16))
+    ids = torch.randint(0, rows, (n,), generator=gen(4)).cuda()
+    out = lookup(table, ids)
+    del big
+    for lo in range(0, n, 100_000):
+        assert torch.equal(out[lo:lo + 100_000], table[ids[lo:lo + 100_000]])
+    by = RowOrder(n, rows, width)
+    by.sort(ids)
+    got = by.lookup_grad(out, dtype=F32)
+    count = torch.bincount(ids, minlength=rows)
+    assert torch.equal(got, table.float() * count[:, None])   # whole numbers below 2^24: exact in FP32

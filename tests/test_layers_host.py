@@ -138,7 +138,17 @@ def test_workspaces():
             refused(fn, *args)
     assert B.gro_row_sort_workspace(0, 0) == 0 and B.gro_row_sort_workspace(8192, 1000) == 0
     sizes = [B.gro_row_sort_workspace(n, r) for n, r in ((8193, 0), (8193, 1000), (8193, 2000), (1 << 20, 2000), (2 ** 31 - 2 ** 16, 2000))]
-    assert sizes == sorted(sizes) and all(s >= 8 * 8193 for s in sizes) and sizes[-1] >= 8 * (2 ** 31 - 2 ** 16)
+    assert sizes == sorted(sizes) and all(s >= 8 * 8193 for s in sizes[2:]) and sizes[-1] >= 8 * (2 ** 31 - 2 ** 16)
+
+
+def test_a_workspace_serves_shorter_lists():
+    lengths = sorted(m + d for m in (511, 4096, 8192, 65_536, 131_072, 1 << 20, 1 << 21) for d in (-1, 0, 1, 4096))
+    for rows in (0, 3, 1000, 1024, 1025, 30_000, 1 << 20):
+        sizes = [B.gro_row_sort_workspace(n, rows) for n in lengths]
+        assert sizes == sorted(sizes)
+    for cols in (0, 1, 2048):
+        sizes = [B.gro_lookup_grad_workspace(n, cols) for n in lengths]
+        assert sizes == sorted(sizes)
 
 
 @pytest.fixture
