@@ -33,7 +33,9 @@ import sys
 from collections import defaultdict
 
 OURS = ("k_accumulate_window", "k_accumulate", "k_adamw_coded", "k_adamw", "k_norm_partials", "k_norm_final",
-        "k_moments_encode", "k_moments_decode", "k_group_norm", "k_group_adamw")
+        "k_moments_encode", "k_moments_decode", "k_group_norm", "k_group_adamw", "k_row_sort_few", "k_row_sort_count",
+        "k_row_sort_spread", "k_row_sort_bucket", "k_lookup", "k_grad_runs", "k_grad_rows", "k_experts_tiles",
+        "k_experts_join")
 CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc")
 
 
