@@ -214,6 +214,29 @@ def test_gradients_against_differences():
     assert dx.shape == x.shape and dw.shape == w.shape
 
 
+def whole(seed, most, *shape):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g).to(BF16)
+
+
+@pytest.mark.parametrize("name", ["small odd", "eights", "around tiles", "many experts", "few rows, long sums", "a round and a few tiles"])
+def test_gradients_equal_differences(name):
+    """d sum(y * r) along a direction, by the forward product at two points.  All values are whole: |y| is at most
+    2 * 3 * 2,056, |dx| 4 * 2,100 and |dw| 4 * 8,357, below 2^24, so every FP32 sum is exact in any order, and so are
+    the 64-bit ones of at most 2^25 terms below 2^16; nothing is left for a tolerance."""
+    c = Case(name)
+    x, w, r = whole(31, 2, c.rows, c.inner).cuda(), whole(32, 2, c.n, c.outer, c.inner).cuda(), whole(33, 2, c.rows, c.outer).cuda()
+    dx = L.experts_input_grad(r, w, c.dstarts, dtype=F32).double()
+    dw = L.experts_weight_grad(r, x, c.dstarts, dtype=F32).double()
+    f = lambda x, w: (L.experts_forward(x, w, c.dstarts, dtype=F32).double() * r.double()).sum()  # noqa: E731
+    for seed in (34, 36, 38):
+        ex, ew = whole(seed, 1, *x.shape).cuda(), whole(seed + 1, 1, *w.shape).cuda()
+        for got, change in (((f(x + ex, w) - f(x - ex, w)) / 2, (dx * ex.double()).sum()),
+                            ((f(x, w + ew) - f(x, w - ew)) / 2, (dw * ew.double()).sum())):
+            assert float(change) != 0 and float(got) == float(change), (name, seed)
+
+
 def test_captured_and_replayed():
     """Runs' lengths are read on the device: a replay follows the starts of its time."""
     c = Case("batch", 40)

@@ -156,6 +156,25 @@ def test_lookup_grad(n, rows, width, kind):
             assert out.rest_untouched() and d.rest_untouched()
 
 
+@pytest.mark.parametrize("n,rows,width,kind", [(5, 3, 33, "mixed"), (700, 40, 333, "mixed"), (5_000, 9, 64, "one"), (9_000, 3_000, 72, "few")])
+def test_gradient_equals_differences(n, rows, width, kind):
+    """d sum(out * r) along a direction, by the lookup at two points.  All values are whole and the scale is 4, so a
+    row's sum is at most 9,000 * 2 * 4, below 2^24: every FP32 sum is exact in any order, as are the 64-bit ones."""
+    g = gen(n)
+    whole = lambda most, *shape: torch.randint(-most, most + 1, shape, generator=g).to(BF16).cuda()  # noqa: E731
+    ids = draw_ids(n, rows, n, kind).cuda()
+    table, r = whole(2, rows, width), whole(2, n, width)
+    by_row = RowOrder(n, rows, width)
+    by_row.sort(ids)
+    dw = by_row.lookup_grad(r, 4.0, dtype=F32).double()
+    f = lambda t: (lookup(t, ids, 4.0, dtype=F32).double() * r.double()).sum()  # noqa: E731
+    for _ in range(3):
+        e = whole(1, rows, width)
+        change = (dw * e.double()).sum()
+        got = (f(table + e) - f(table - e)) / 2
+        assert float(change) != 0 and float(got) == float(change)
+
+
 def test_infinities_and_nan_stay_in_their_rows():
     n, rows, width = 600, 5, 40
     ids = torch.arange(n) % 4
