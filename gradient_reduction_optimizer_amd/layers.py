@@ -175,7 +175,7 @@ class RowOrder:
         ``dtype``, by default dy's."""
         if dy.dim() < 2:
             raise ValueError(f"dy: a row for each id is needed, got {tuple(dy.shape)}")
-        flat = dy if dy.dim() == 2 else dy.reshape(-1, dy.shape[-1])
+        flat = dy if dy.dim() == 2 else dy.flatten(0, -2)
         d = _matrix("dy", flat, self._gpu)
         if accumulate and out is None:
             raise ValueError("accumulate adds to an array that is given")

@@ -240,6 +240,29 @@ def test_python_calls_hand_over_what_the_tensors_are(on_gpu):
     assert L.lookup(bf(20, 8), ids).shape == (4, 3, 8)
 
 
+def test_rows_without_elements(on_gpu):
+    """A gradient of width 0 in the ids' shape has a row for each id all the same."""
+    by = L.RowOrder(6, 10, 0)
+    by.sort(torch.zeros(2, 3, dtype=torch.int64))
+    assert L.lookup(bf(10, 0), torch.zeros(2, 3, dtype=torch.int64)).shape == (2, 3, 0)
+    for dy in (bf(2, 3, 0), bf(6, 0), bf(1, 2, 3, 0)):
+        assert by.lookup_grad(dy).shape == (10, 0)
+        _, (d, *_) = on_gpu.pop()
+        assert (d.rows, d.cols) == (6, 0)
+    by.sort(torch.zeros(0, 3, dtype=torch.int64))
+    assert by.lookup_grad(bf(0, 3, 0)).shape == (10, 0)
+    with pytest.raises(ValueError):
+        by.lookup_grad(bf(2, 3, 0))
+    # and several rows of a width, contiguous and not
+    by = L.RowOrder(6, 10, 8)
+    by.sort(torch.zeros(2, 3, dtype=torch.int64))
+    base = bf(2, 6, 8)
+    for dy, stride in ((base[:, ::2], 16), (base[:, :3], 8), (bf(2, 3, 8), 8), (bf(3, 2, 8).transpose(0, 1), 8)):
+        by.lookup_grad(dy)
+        _, (d, *_) = on_gpu.pop()
+        assert (d.rows, d.cols, d.stride) == (6, 8, stride)
+
+
 def test_a_view_of_a_gradient_slot():
     plan = Plan([dict(param_id=0, shape=(30, 4), placement="replicate"), dict(param_id=1, shape=(100, 8), placement="shard",
                                                                               shard_index=0),
