@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t b, uint32_t total, uint32
   return c > 0 ? (j / c * 8 + (b & 7)) * c + j % c : 0;
 }
 // Numbers b that reach every tile so.
-__host__ __device__ inline uint32_t xcd_numbers(uint32_t total, uint32_t chunk) { return (total + 7) / 8 * 8 + 8 * chunk; }
+__device__ __forceinline__ uint32_t xcd_numbers(uint32_t total, uint32_t chunk) { return (total + 7) / 8 * 8 + 8 * chunk; }
 
 // Number `i` of a grid of m_tiles x n_tiles in bands of up to 8 tiles of m: neighbours
 // in number are neighbours in both.
@@ -132,8 +132,12 @@ constexpr int kStepK = 32, kStages = 4;
 // LDS of a workgroup: four steps of both operands, and for each wave a block of 32 x 32
 // results.
 constexpr int tile_lds(int bm, int bn, int waves) { return (bm + bn) * kStepK * 2 * kStages + waves * 32 * 32 * 4; }
-// Workgroups of a compute unit, and tiles that an XCD's 32 units work on at a time.
+// Workgroups of a compute unit, tiles that an XCD's 32 units work on at a time, and the
+// launch: the kernel steps from tile to tile by so many, so a launch has all of them,
+// also for fewer tiles.
 constexpr int tile_units(int bm, int bn, int waves) { return 160 * 1024 / tile_lds(bm, bn, waves); }
+constexpr uint32_t tile_chunk(int bm, int bn, int waves) { return 32 * uint32_t(tile_units(bm, bn, waves)); }
+constexpr uint32_t tile_grid(int bm, int bn, int waves) { return 8 * tile_chunk(bm, bn, waves); }
 
 // One operand's tile of R rows (of C) and 32 k.
 //   k innermost in memory (T = false): LDS holds [R][32], row r's chunk c of 8
@@ -384,7 +388,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_experts_tiles(const Experts
   constexpr bool CF = C == kFp32, PARTS = COVER == kParts, QUARTERS = COVER == kQuarters;
   constexpr int TM = QUARTERS ? 2 * BM : BM, TN = QUARTERS ? 2 * BN : BN;  // as tiles are numbered
   constexpr bool AT = MODE == kWeightGrad, BT = MODE != kForward;
-  constexpr uint32_t kChunk = 32 * tile_units(BM, BN, WM * WN), kGrid = 8 * kChunk;
+  constexpr uint32_t kChunk = tile_chunk(BM, BN, WM * WN), kGrid = tile_grid(BM, BN, WM * WN);
   __shared__ __attribute__((aligned(16))) uint16_t a0[BM * kStepK], a1[BM * kStepK], a2[BM * kStepK], a3[BM * kStepK];
   __shared__ __attribute__((aligned(16))) uint16_t b0[BN * kStepK], b1[BN * kStepK], b2[BN * kStepK], b3[BN * kStepK];
   __shared__ __attribute__((aligned(16))) float results[WM * WN][32 * 32];
@@ -710,9 +714,7 @@ bool direct(const ExpertsLaunch& a, ExpertsMode mode) {
 
 template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER = kAll>
 hipError_t tiles(const ExpertsLaunch& a, hipStream_t s) {
-  constexpr uint32_t units = tile_units(BM, BN, WM * WN);
-  const uint32_t n = COVER == kQuarters ? 256 * units : xcd_numbers(uint32_t(tiles_of(a, ExpertsMode(MODE), BM, BN)), 32 * units);
-  const dim3 grid(std::min(n, 256 * units)), block(64 * WM * WN);
+  const dim3 grid(tile_grid(BM, BN, WM * WN)), block(64 * WM * WN);
   const bool lines = ((reinterpret_cast<uintptr_t>(a.c) | uint64_t(2 * a.c_stride) | uint64_t(2 * a.c_expert)) & 127) == 0;
   if (a.c_fp32) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, kFp32>), grid, block, 0, s, a);
   else if (DIRECT && lines) hipLaunchKernelGGL((k_experts_tiles<MODE, BM, BN, WM, WN, DIRECT, COVER, DIRECT ? kBf16Lines : kBf16>), grid, block, 0, s, a);
@@ -729,9 +731,7 @@ hipError_t in_parts(const ExpertsLaunch& a, hipStream_t s) {
   b.accumulate = 0;
   b.c_stride = MODE == kForward ? a.outer : a.inner;
   b.c_expert = a.outer * a.inner;
-  constexpr uint32_t units = tile_units(128, 128, 4);
-  const uint32_t n = uint32_t(tiles_of(a, ExpertsMode(MODE), 128, 128));
-  const dim3 places(std::min(xcd_numbers(n * uint32_t(a.n_parts), 32 * units), 256 * units)), grid(n * (128 / kJoinRows));
+  const dim3 places(tile_grid(128, 128, 4)), grid(uint32_t(tiles_of(a, ExpertsMode(MODE), 128, 128)) * (128 / kJoinRows));
   hipLaunchKernelGGL((k_experts_tiles<MODE, 128, 128, 2, 2, DIRECT, kParts, kFp32>), places, dim3(256), 0, s, b);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

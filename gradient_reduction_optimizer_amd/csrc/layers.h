@@ -133,9 +133,10 @@ struct ExpertsLaunch {
   float* partials;          // [n_parts][C without gaps]
   int64_t c_part;           // elements of one part
 };
-// The most workgroups that a call launches (a launch has fewer than 2^32 lanes).
+// Tiles of 128 x 128 that a product takes at most, and may: the kernels number them, and
+// some numbers that stand for none, in 32 bits.
 int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode);
-constexpr int64_t kMaxExpertsTiles = (int64_t(1) << 23) - 1;
+constexpr int64_t kMaxExpertsTiles = int64_t(1) << 31;
 int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inner, int64_t outer);
 hipError_t launch_experts(const ExpertsLaunch& a, ExpertsMode mode, hipStream_t s);
 

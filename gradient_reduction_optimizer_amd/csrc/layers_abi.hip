@@ -212,7 +212,7 @@ int run_product(const gro_matrix* in, const gro_experts* w, const int32_t* start
   a.n_parts = parts;
   a.partials = static_cast<float*>(d_workspace);
   a.c_part = in->rows * to;
-  if (experts_tiles(a, mode) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product too large for one launch");
+  if (experts_tiles(a, mode) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product of too many tiles");
   const hipError_t e = launch_experts(a, mode, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GRO_OK : hip_fail(e, "experts' product launch");
 }
@@ -421,7 +421,7 @@ extern "C" int gro_experts_weight_grad(const gro_matrix* dy, const gro_matrix* x
   a.partials = static_cast<float*>(d_workspace);
   a.n_parts = parts;
   a.c_part = elems;
-  if (experts_tiles(a, kWeightGrad) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product too large for one launch");
+  if (experts_tiles(a, kWeightGrad) > kMaxExpertsTiles) return set_error(GRO_E_INVALID, "product of too many tiles");
   const hipError_t e = launch_experts(a, kWeightGrad, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? GRO_OK : hip_fail(e, "experts' weight gradient launch");
 }

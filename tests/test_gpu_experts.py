@@ -379,3 +379,18 @@ def test_places_past_32_bits():
     for e, (lo, hi) in enumerate(((0, 10_000), (10_000, m - 20), (m - 20, m))):
         want = dy[lo:hi].double().t() @ far[lo:hi].double()
         assert torch.equal(dw[e], want.to(BF16))               # FP32 sums below 2^24 are exact, rounded once
+
+
+def test_more_tiles_than_a_launch_has_lanes_for():
+    """2^23 and more tiles of 128 rows, which the workgroups take one after the other: rows of one element, whose
+    products by a power of two are exact."""
+    cut, n = (1 << 30) - 77, (1 << 30) + 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    x = torch.randint(-3, 4, (n, 1), generator=g, dtype=torch.int8, device="cuda").to(BF16)
+    w = torch.tensor([2.0, -0.5], device="cuda").to(BF16).view(2, 1, 1)
+    starts = torch.tensor([0, cut, n], dtype=torch.int32).cuda()
+    y = L.experts_forward(x, w, starts)
+    assert torch.equal(y[:cut], x[:cut] * 2) and torch.equal(y[cut:], x[cut:] * -0.5)
+    dx = L.experts_input_grad(x, w, starts, out=y.fill_(9))
+    assert torch.equal(dx[:cut], x[:cut] * 2) and torch.equal(dx[cut:], x[cut:] * -0.5)
