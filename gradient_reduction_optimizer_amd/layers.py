@@ -15,11 +15,15 @@ A call runs on ``stream``, by default the current one; ordering it after the wor
 that made its inputs is the caller's, as with any operation on another stream.
 Memory is not: what a call uses on a stream other than the current one is kept until
 that stream is done with it.  Nothing here takes part in autograd: forward and
-gradient are calls of their own.
+gradient are calls of their own.  Tensors whose gradient autograd would lose that
+way are refused while it records (those that require one, and those with a
+forward-mode tangent): call under ``torch.no_grad()`` or with detached tensors, or
+from a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as B
 
@@ -27,8 +31,19 @@ _TYPES = {torch.bfloat16: B.GRO_BF16, torch.float32: B.GRO_FP32}
 _IDS = {torch.int32: B.GRO_INT32, torch.int64: B.GRO_INT64}
 
 
+def _not_recorded(what: str, t) -> None:
+    """Nothing that autograd follows would be lost in a call that it does not see."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and the layers take no part in autograd: call under torch.no_grad() "
+                         f"or with detached tensors")
+    # a tangent needs a level that is entered; without one this is all there is to look at
+    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{what} has a forward-mode tangent, which the layers' results would not have")
+
+
 def _matrix(what: str, t, device, dtypes=_TYPES) -> B.gro_matrix:
     """A matrix of one of these types on this GPU (its index) whose rows' elements lie side by side."""
+    _not_recorded(what, t)
     kind = dtypes.get(t.dtype)
     shape = t.shape
     if len(shape) != 2 or kind is None or t.get_device() != device or (shape[1] > 1 and t.stride(1) != 1):
@@ -39,6 +54,7 @@ def _matrix(what: str, t, device, dtypes=_TYPES) -> B.gro_matrix:
 
 
 def _experts(what: str, t, device, dtypes=_TYPES) -> B.gro_experts:
+    _not_recorded(what, t)
     kind = dtypes.get(t.dtype)
     if t.dim() != 3 or kind is None or t.get_device() != device or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError(f"{what}: [experts, outer, inner] of {' or '.join(map(str, dtypes))} on cuda:{device}, rows' "

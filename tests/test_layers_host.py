@@ -240,6 +240,80 @@ def test_python_calls_hand_over_what_the_tensors_are(on_gpu):
     assert L.lookup(bf(20, 8), ids).shape == (4, 3, 8)
 
 
+def every_call(t, rows=lambda: bf(5, 8), back=lambda: bf(5, 16), matrices=lambda: bf(3, 16, 8)):
+    """Each call with one of its tensors made by ``t``, and which: inputs and results."""
+    ids, starts = torch.zeros(5, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)
+    by = L.RowOrder(5, 10, 8)
+    by.sort(ids)
+    return {"table": lambda: L.lookup(t(bf(10, 8)), ids), "rows": lambda: L.lookup(bf(10, 8), ids, out=t(rows())),
+            "dy": lambda: by.lookup_grad(t(rows())), "dy of the ids' shape": lambda: by.lookup_grad(t(bf(1, 5, 8))),
+            "row gradient": lambda: by.lookup_grad(rows(), out=t(bf(10, 8))),
+            "x": lambda: L.experts_forward(t(rows()), matrices(), starts), "w": lambda: L.experts_forward(rows(), t(matrices()), starts),
+            "y": lambda: L.experts_forward(rows(), matrices(), starts, out=t(back())),
+            "dy of rows": lambda: L.experts_input_grad(t(back()), matrices(), starts),
+            "dx": lambda: L.experts_input_grad(back(), matrices(), starts, out=t(rows())),
+            "dy of weights": lambda: L.experts_weight_grad(t(back()), rows(), starts),
+            "x of weights": lambda: L.experts_weight_grad(back(), t(rows()), starts),
+            "dw": lambda: L.experts_weight_grad(back(), rows(), starts, out=t(matrices()))}
+
+
+def test_a_gradient_that_autograd_would_lose_is_refused(on_gpu):
+    """The results take no part in autograd's graph: what would have to is refused, as torch refuses it for out=, and
+    taken where nothing is recorded."""
+    by = every_call(lambda t: t.requires_grad_())
+    del on_gpu[:]
+    for name, call in by.items():
+        with pytest.raises(ValueError, match="autograd"):
+            call()
+        assert not on_gpu, name
+        with torch.no_grad():
+            call()
+        with torch.inference_mode():
+            call()
+        assert len(on_gpu) == 2, name
+        del on_gpu[:]
+    for call in every_call(lambda t: t.requires_grad_().detach()).values():
+        call()
+    # so are they in an operation of the caller's own, whose forward and backward are recorded as one
+    ids = torch.zeros(5, dtype=torch.int64)
+
+    class Lookup(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, table):
+            return L.lookup(table, ids)
+
+        @staticmethod
+        def backward(ctx, dy):
+            order = L.RowOrder(5, 10, 8)
+            order.sort(ids)
+            return order.lookup_grad(dy)
+
+    table = bf(10, 8).requires_grad_()
+    Lookup.apply(table).float().square().sum().backward()
+    assert table.grad.shape == (10, 8)
+
+
+@pytest.fixture
+def forward_mode():
+    """torch compiles its own formulas for it at the first level, which it cannot once functions are replaced."""
+    from torch.autograd import forward_ad
+    with forward_ad.dual_level():
+        forward_ad.make_dual(torch.zeros(1), torch.ones(1))
+    return forward_ad
+
+
+def test_a_tangent_is_refused(forward_mode, on_gpu):
+    forward_ad = forward_mode
+    with forward_ad.dual_level():
+        for name, call in every_call(lambda t: forward_ad.make_dual(t, torch.ones_like(t))).items():
+            del on_gpu[:]
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+            assert not on_gpu, name
+        for call in every_call(lambda t: t).values():
+            call()
+
+
 def test_rows_without_elements(on_gpu):
     """A gradient of width 0 in the ids' shape has a row for each id all the same."""
     by = L.RowOrder(6, 10, 0)
