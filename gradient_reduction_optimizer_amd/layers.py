@@ -22,6 +22,8 @@ from a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
+import types
+
 import torch
 from torch.autograd import forward_ad
 
@@ -31,30 +33,35 @@ _TYPES = {torch.bfloat16: B.GRO_BF16, torch.float32: B.GRO_FP32}
 _IDS = {torch.int32: B.GRO_INT32, torch.int64: B.GRO_INT64}
 
 
+# No tensor has a tangent while no level is entered (-1); a torch that does not say is asked of every tensor.
+_levels = forward_ad if hasattr(forward_ad, "_current_level") else types.SimpleNamespace(_current_level=0)
+
+
 def _not_recorded(what: str, t) -> None:
     """Nothing that autograd follows would be lost in a call that it does not see."""
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{what} requires a gradient, and the layers take no part in autograd: call under torch.no_grad() "
                          f"or with detached tensors")
-    # a tangent needs a level that is entered; without one this is all there is to look at
-    if getattr(forward_ad, "_current_level", 0) >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+    if forward_ad.unpack_dual(t).tangent is not None:
         raise ValueError(f"{what} has a forward-mode tangent, which the layers' results would not have")
 
 
 def _matrix(what: str, t, device, dtypes=_TYPES) -> B.gro_matrix:
     """A matrix of one of these types on this GPU (its index) whose rows' elements lie side by side."""
-    _not_recorded(what, t)
+    if t.requires_grad or _levels._current_level >= 0:
+        _not_recorded(what, t)
     kind = dtypes.get(t.dtype)
-    shape = t.shape
-    if len(shape) != 2 or kind is None or t.get_device() != device or (shape[1] > 1 and t.stride(1) != 1):
+    shape, step = t.shape, t.stride()
+    if len(shape) != 2 or kind is None or t.get_device() != device or (shape[1] > 1 and step[1] != 1):
         raise ValueError(f"{what}: a matrix of {' or '.join(map(str, dtypes))} on cuda:{device}, rows' elements side by "
-                         f"side, is needed, got {t.dtype} {tuple(shape)}, strides {t.stride()}, on {t.device}")
+                         f"side, is needed, got {t.dtype} {tuple(shape)}, strides {step}, on {t.device}")
     rows, cols = shape
-    return B.gro_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else cols, kind, 0)
+    return B.gro_matrix(t.data_ptr(), rows, cols, step[0] if rows > 1 else cols, kind, 0)
 
 
 def _experts(what: str, t, device, dtypes=_TYPES) -> B.gro_experts:
-    _not_recorded(what, t)
+    if t.requires_grad or _levels._current_level >= 0:
+        _not_recorded(what, t)
     kind = dtypes.get(t.dtype)
     if t.dim() != 3 or kind is None or t.get_device() != device or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError(f"{what}: [experts, outer, inner] of {' or '.join(map(str, dtypes))} on cuda:{device}, rows' "
@@ -103,9 +110,12 @@ def _call(device, stream, tensors, made, fn, *args) -> None:
             fn(*args, s.cuda_stream)
 
 
+_count = torch.autograd.graph.increment_version
+
+
 def _wrote(out) -> None:
     """An operation in place on the caller's tensor, as autograd counts them."""
-    torch.autograd.graph.increment_version(out)
+    _count(out)
 
 
 def _aligned(room) -> int:
