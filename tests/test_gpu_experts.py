@@ -394,3 +394,20 @@ def test_more_tiles_than_a_launch_has_lanes_for():
     assert torch.equal(y[:cut], x[:cut] * 2) and torch.equal(y[cut:], x[cut:] * -0.5)
     dx = L.experts_input_grad(x, w, starts, out=y.fill_(9))
     assert torch.equal(dx[:cut], x[:cut] * 2) and torch.equal(dx[cut:], x[cut:] * -0.5)
+
+
+def test_experts_held_apart():
+    """Experts that are parameters of their own: a call for each, with its two entries of the starts."""
+    c = Case("eights", 80)
+    x, dy = c.x.cuda(), c.dy.cuda()
+    y, dx = torch.zeros(c.rows, c.outer).cuda(), torch.zeros(c.rows, c.inner).cuda()
+    for e, at in c.runs():
+        w, dw, two = c.w[e:e + 1].cuda(), torch.full((1, c.outer, c.inner), 3.0).cuda(), c.dstarts[e:e + 2]
+        L.experts_forward(x, w, two, out=y)
+        L.experts_input_grad(dy, w, two, out=dx)
+        L.experts_weight_grad(dy, x, two, out=dw)
+        R.check_close(dw[0], *R.product(c.dy[at].t(), c.x[at]), e)
+    for e, at in c.runs():
+        R.check_close(y[at], *R.product(c.x[at], c.w[e].t()), e)
+        R.check_close(dx[at], *R.product(c.dy[at], c.w[e]), e)
+    assert bool((y[c.rows - c.behind:] == 0).all()) and bool((dx[c.rows - c.behind:] == 0).all())
