@@ -118,12 +118,12 @@ struct Tiles {
 // this one's result is written.  All tiles end at about the same time, and their results
 // leave in bursts that the memory takes 6 us for, 10 us a tile with what else it costs to
 // begin one: without that 2048 k would run at 1.3 PFLOP/s.
-//   32,768 rows of 16 experts from 2048 to 8192 elements: 1,062 us forward (1.04
+//   32,768 rows of 16 experts from 2048 to 8192 elements: 1,069 us forward (1.03
 // PFLOP/s; the ragged tiles are 6 % of the work), 16,384 rows of 8 experts of 1024 x 4096
-// 150 us for the input gradient (k = 1024: 0.92) and 140 for the weight gradient (0.98);
+// 151 us for the input gradient (k = 1024: 0.91) and 136 for the weight gradient (1.01);
 // the matrix cores are busy for 63, 57 and (FP32 results added to) 48 % of the cycles, LDS
-// for 26, 34 and 40.  A library product of the first one's size with a single matrix runs
-// at 1.22 to 1.27.
+// for 26, 34 and 40.  Library products of the first two's sizes with a single matrix, the
+// operands in these orders, run at 1.34 to 1.47 and 1.09.
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -377,9 +377,9 @@ __device__ __forceinline__ uint32_t left_over(uint32_t total) {
 
 // C in FP32, in BF16, or in BF16 with rows that begin at whole lines of 128 bytes.  The
 // last are stored past the caches, since C is larger than they are and the next tiles'
-// operands are in them: an input gradient of 16,384 rows 136 us instead of 157.  Pieces
-// of lines are left to the caches: 48 weight gradients of 1408 x 3944 without a row each
-// 199 us instead of 345.  FP32 takes the same time either way.
+// operands are in them: an input gradient of 16,384 rows 136 us instead of 157, the same
+// inputs in turn.  Pieces of lines are left to the caches: 48 weight gradients of 1408 x
+// 3944 without a row each 199 us instead of 345.  FP32 takes the same time either way.
 enum Result { kFp32, kBf16, kBf16Lines };
 
 template <int MODE, int BM, int BN, int WM, int WN, bool DIRECT, int COVER, int C>
@@ -748,7 +748,8 @@ hipError_t product(const ExpertsLaunch& a, hipStream_t s) {
   // Large tiles where an expert's rows and its columns of C are most of one and three
   // quarters of the GPU have one.  us, large against small, 16 experts from 2048 to 2048:
   // 64 rows each 45 / 26, 128 46 / 27, 256 51 / 47, 384 70 / 81, 512 69 / 86; 8 experts of
-  // 2048 rows from 1024 to 256, 64 large tiles: 27 / 15.
+  // 2048 rows from 1024 to 256, 64 large tiles: 27 / 15.  All with experts of equal length:
+  // the host knows the runs' average alone.
   const int64_t n = MODE == kForward ? a.outer : a.inner, m = MODE == kWeightGrad ? a.outer : a.rows / a.n_experts;
   const int64_t most = tiles_of(a, ExpertsMode(MODE), 256, 256);
   if (m <= 192 || n <= 192 || most < 192) return tiles<MODE, 128, 128, 2, 2, true>(a, s);
@@ -773,6 +774,8 @@ int64_t experts_tiles(const ExpertsLaunch& a, ExpertsMode mode) { return tiles_o
 // (0.2 us each) are more than the join costs (5 us and the parts' traffic).  us, whole
 // against parts, to 1024: 128 rows of one expert from 4096 30 / 15, from 1024 11.5 / 13.4
 // (so whole); 16 rows each of 4 experts from 2048 17 / 13, of 16 experts 18 / 22 (whole).
+// A weight gradient's k are an expert's rows, of which the host knows the average alone:
+// 32,768 rows of 64 experts of 256 x 256 12 us, with half of them in one 111.
 int experts_parts(ExpertsMode mode, int32_t n_experts, int64_t rows, int64_t inner, int64_t outer) {
   if (n_experts <= 0 || rows <= 0 || inner <= 0 || outer <= 0) return 1;
   ExpertsLaunch a = {};
